@@ -354,6 +354,83 @@ csa_status csa_grouped_out_proj(const void *o, const void *Wg, const void *Wo, i
                                 int c, int g, int dg, int d, void *u, void *out, void *stream);
 
 /*
+ * The 8-bit projections of a layer: three calls that bring the hidden state to
+ * the path's operands (Module B steps 1-3: C^a .. Z^b = H W, c^Q = H W^{DQ},
+ * q^I = c^Q W^{IUQ}, w^I = H W^w, q = c^Q W^{UQ}) and the heads to the output
+ * (step 4) with e4m3 operands. Storage rule of all three, that of the entries
+ * above: a block of values shares one float32 scale max(amax / 448, 2^-126),
+ * codes are value / scale rounded to nearest even. Activations [rows, d] have
+ * a scale per row and 128 channels, [rows, ceil(d / 128)] (the last block may
+ * be cut); weights [N, K] (output features by input features) one per block of
+ * 128 features x 128 inputs, [ceil(N / 128), ceil(K / 128)]. The pages fix the
+ * 8-bit storage of the path but neither block sizes nor the projections'
+ * precision; these are this library's.
+ *
+ * csa_add_norm_quant -- residual addition, RMSNorm and e4m3 output in one pass:
+ *   s = x + residual                           (s = x without residual)
+ *   v = s / sqrt(mean_j s_j^2 + eps) * gamma   (v = s when !normalise)
+ *   total <- s, y <- v, (codes, scale) <- v
+ * all in float32 until the one rounding of each output (the norm reads s
+ * before it is rounded to total).
+ * Arguments:
+ *   x         [rows, d] of dt (F32 or BF16).
+ *   residual  [rows, d] of dt, or NULL.
+ *   gamma     [d] float32, or NULL for a gain of 1; NULL when !normalise.
+ *   total     [rows, d] of dt, or NULL; needs residual, and may be the same
+ *             buffer as residual or x.
+ *   y         [rows, d] of dt, or NULL; may be the same buffer as x.
+ *   codes     [rows, d] e4m3, and scale [rows, ceil(d / 128)] float32: both or
+ *             neither. At least one of total, y and codes is given.
+ * Other overlaps of outputs with inputs or outputs are not allowed. A NaN
+ * makes the whole row's y and codes NaN when normalising, else the codes and
+ * scale of its block; an infinity gives its block the scale +inf (and, when
+ * normalising, zeros beside a NaN).
+ * Requirements: d a multiple of 16, 16 <= d <= 65536; eps > 0 when
+ *   normalising; x, residual, total, y and codes 16-byte aligned. rows = 0 is
+ *   a no-op.
+ */
+csa_status csa_add_norm_quant(const void *x, const void *residual, const float *gamma,
+                              csa_dtype dt, int64_t rows, int d, int normalise, float eps,
+                              void *total, void *y, void *codes, float *scale, void *stream);
+
+/*
+ * csa_quantize_weight -- a weight in the form csa_fp8_proj reads: W [N, K] of
+ * dt (F32 or BF16) to codes [N, K] e4m3 and scale [ceil(N / 128),
+ * ceil(K / 128)] float32. A NaN reaches its whole block.
+ * Requirements: N >= 0 (0 is a no-op); K a multiple of 16, K >= 16; W and
+ *   codes 16-byte aligned; no overlap.
+ */
+csa_status csa_quantize_weight(const void *W, csa_dtype dt, int64_t N, int K, void *codes,
+                               float *scale, void *stream);
+
+/*
+ * csa_fp8_proj -- product of e4m3 activations and weights with block scales,
+ * for `groups` independent groups (1: a plain projection; the grouped output
+ * projection of step 4 with groups = g):
+ *   r[t, g N + j] = sum_b As[t, g nb + b] Ws[(g N + j) / 128, b]
+ *                   sum_{k in block b} A[t, g K + k] W[g N + j, k]
+ * with b over the nb = ceil(K / 128) blocks of the inputs; products and sums
+ * in float32.
+ * Arguments:
+ *   A, A_scale  [M, groups K] e4m3 and [M, groups nb] float32.
+ *   W, W_scale  [groups N, K] e4m3 and [ceil(groups N / 128), nb] float32.
+ *   out         [M, groups N] of out_dt: F32, BF16 (one rounding of r), or
+ *               E4M3 with out_scale [M, ceil(groups N / 128)] float32 (the
+ *               storage rule over 128 columns of r: with head width 128 these
+ *               are the indexer queries and their qI_scale). out_scale is NULL
+ *               for the other types.
+ * A row's result does not depend on the values of other rows, and the same call
+ * gives the same bits; M may choose another order of the sums.
+ * Requirements: 0 <= M <= INT32_MAX (0 is a no-op); N >= 1; K a multiple of
+ *   16, K >= 16; groups >= 1, and N and K multiples of 128 when groups > 1;
+ *   N a multiple of 16 for E4M3; groups N and groups K at most INT32_MAX; A, W
+ *   and out 16-byte aligned; out and out_scale overlap no other operand.
+ */
+csa_status csa_fp8_proj(const void *A, const float *A_scale, const void *W, const float *W_scale,
+                        int64_t M, int N, int K, int groups, csa_dtype out_dt, void *out,
+                        float *out_scale, void *stream);
+
+/*
  * csa_debug_wait_probe -- checks the device-side failure path. Launches one
  * thread that waits, through the same bounded mbarrier wait every pipeline
  * kernel uses, on a barrier that nothing completes; after limit_ns

@@ -30,6 +30,7 @@ EXPORTS = ("csa_abi_version", "csa_status_string", "csa_last_message", "csa_comp
            "csa_indexer_topk_workspace_size", "csa_indexer_topk_launches", "csa_sparse_mqa",
            "hca_dense_mqa", "csa_mqa_workspace_size", "csa_sparse_mqa_noalloc",
            "csa_noalloc_scratch_bytes", "csa_norm_rope", "csa_grouped_out_proj",
+           "csa_add_norm_quant", "csa_quantize_weight", "csa_fp8_proj",
            "csa_debug_wait_probe", "csa_get_error")
 
 
@@ -98,6 +99,12 @@ def load(path: str = LIB_PATH):
     L.csa_norm_rope.argtypes = [_P, _I, _P, _I64, _I, _I, _I, _P, _I64, _I64, _I, _F, _F, _P]
     L.csa_grouped_out_proj.restype = _I
     L.csa_grouped_out_proj.argtypes = [_P, _P, _P, _I64, _I, _I, _I, _I, _I, _P, _P, _P]
+    L.csa_add_norm_quant.restype = _I
+    L.csa_add_norm_quant.argtypes = [_P, _P, _P, _I, _I64, _I, _I, _F, _P, _P, _P, _P, _P]
+    L.csa_quantize_weight.restype = _I
+    L.csa_quantize_weight.argtypes = [_P, _I, _I64, _I, _P, _P, _P]
+    L.csa_fp8_proj.restype = _I
+    L.csa_fp8_proj.argtypes = [_P, _P, _P, _P, _I64, _I, _I, _I, _I, _P, _P, _P]
     L.csa_debug_wait_probe.restype = _I
     L.csa_debug_wait_probe.argtypes = [ctypes.c_uint64, _P]
     L.csa_get_error.restype = _I
@@ -273,6 +280,93 @@ def csa_grouped_out_proj(o, Wg, Wo, g: int, u, out, stream=None):
     d = Wo.shape[0]
     _check(load().csa_grouped_out_proj(_ptr(o), _ptr(Wg), _ptr(Wo), n, h, c, g, dg, d, _ptr(u),
                                        _ptr(out), _stream(stream)))
+
+
+def _operands(what: str, *named):
+    """Checks (name, tensor or None, dtypes, shape) operands of one call: dense
+    CUDA tensors of one device, of a listed dtype and shape. Returns the device
+    index and the pointers (None for None)."""
+    devs, ptrs = set(), []
+    for name, t, dtypes, shape in named:
+        if t is None:
+            ptrs.append(None)
+            continue
+        if t.dtype not in dtypes:
+            raise TypeError("%s: %s is %s" % (what, name, t.dtype))
+        if t.shape != shape:
+            raise ValueError("%s: %s is %s, expected %s" % (what, name, tuple(t.shape), shape))
+        if not t.is_contiguous():
+            raise ValueError("%s: %s must be contiguous" % (what, name))
+        devs.add(t.get_device())
+        ptrs.append(t.data_ptr())
+    dev = devs.pop()
+    if devs or dev < 0:
+        raise ValueError("%s: operands must be on one CUDA device" % what)
+    return dev, ptrs
+
+
+def _call_on(dev: int, fn, *args, stream=None):
+    """Calls fn(*args, stream) with `dev` current (its current stream when none
+    is given)."""
+    if dev == torch.cuda.current_device():
+        _check(fn(*args, _stream(stream)))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, _stream(stream)))
+
+
+_PLAIN = (torch.bfloat16, torch.float32)
+_F32 = (torch.float32,)
+_CODES = (torch.float8_e4m3fn, torch.uint8)
+
+
+def _blocks(n: int) -> int:
+    """Blocks of 128 that n values make."""
+    return (n + 127) // 128
+
+
+def csa_add_norm_quant(x, residual=None, gamma=None, normalise: bool = True, eps: float = 1e-6,
+                       total=None, y=None, codes=None, scale=None, stream=None):
+    """total <- x + residual, its RMSNorm (times gamma) to y and, in e4m3 with
+    a scale per 128 channels, to codes and scale; x [..., d]. Outputs that are
+    None are not written."""
+    shape = tuple(x.shape)
+    d = shape[-1]
+    same = (x.dtype,)
+    dev, (px, pr, pg, pt, py, pc, ps) = _operands(
+        "csa_add_norm_quant", ("x", x, _PLAIN, shape), ("residual", residual, same, shape),
+        ("gamma", gamma, _F32, (d,)), ("total", total, same, shape), ("y", y, same, shape),
+        ("codes", codes, _CODES, shape), ("scale", scale, _F32, shape[:-1] + (_blocks(d),)))
+    _call_on(dev, load().csa_add_norm_quant, px, pr, pg, dtype_code(x), x.numel() // d if d else 0,
+             d, int(bool(normalise)), eps, pt, py, pc, ps, stream=stream)
+
+
+def csa_quantize_weight(W, codes, scale, stream=None):
+    """W [N, K] to e4m3 codes [N, K] with a scale per 128 x 128 block,
+    [ceil(N / 128), ceil(K / 128)]."""
+    N, K = W.shape
+    dev, (pw, pc, ps) = _operands(
+        "csa_quantize_weight", ("W", W, _PLAIN, (N, K)), ("codes", codes, _CODES, (N, K)),
+        ("scale", scale, _F32, (_blocks(N), _blocks(K))))
+    _call_on(dev, load().csa_quantize_weight, pw, dtype_code(W), N, K, pc, ps, stream=stream)
+
+
+def csa_fp8_proj(A, A_scale, W, W_scale, out, out_scale=None, groups: int = 1, stream=None):
+    """out [M, groups N] = A [M, groups K] times W [groups N, K] (group by
+    group), e4m3 operands with block scales; out bf16, f32, or e4m3 codes with
+    out_scale [M, ceil(groups N / 128)]."""
+    M, K = A.shape[0], W.shape[1]
+    GN = W.shape[0]
+    if groups < 1 or GN % groups:
+        raise ValueError("csa_fp8_proj: groups must divide the rows of W")
+    nb = _blocks(K)
+    dev, (pa, pas, pw, pws, po, pos) = _operands(
+        "csa_fp8_proj", ("A", A, _CODES, (M, groups * K)),
+        ("A_scale", A_scale, _F32, (M, groups * nb)), ("W", W, _CODES, (GN, K)),
+        ("W_scale", W_scale, _F32, (_blocks(GN), nb)), ("out", out, _PLAIN + _CODES, (M, GN)),
+        ("out_scale", out_scale, _F32, (M, _blocks(GN))))
+    _call_on(dev, load().csa_fp8_proj, pa, pas, pw, pws, M, GN // groups, K, groups,
+             dtype_code(out), po, pos, stream=stream)
 
 
 def csa_debug_wait_probe(limit_ns: int, stream=None):

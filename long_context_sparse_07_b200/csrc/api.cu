@@ -41,6 +41,7 @@ unsigned *err_word()
 }
 
 bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
+bool aligned4(const void *p) { return ((uintptr_t)p & 3u) == 0; }
 bool pow2(int64_t x) { return x > 0 && (x & (x - 1)) == 0; }
 
 csa_status launched(cudaError_t e, const char *what)
@@ -435,6 +436,94 @@ csa_status csa_grouped_out_proj(const void *o, const void *Wg, const void *Wo, i
         return launched(e, w);
     csa::GemmArgs a2{u, Wo, out, n, d, g * dg, 1, (int64_t)g * dg, d, d, 0, 0, 0};
     return launched(csa::launch_gemm_nt(a2, err, s), w);
+}
+
+csa_status csa_add_norm_quant(const void *x, const void *residual, const float *gamma,
+                              csa_dtype dt, int64_t rows, int d, int normalise, float eps,
+                              void *total, void *y, void *codes, float *scale, void *stream)
+{
+    const char *w = "csa_add_norm_quant";
+    REQUIRE(dt == CSA_F32 || dt == CSA_BF16, CSA_ERR_UNSUPPORTED, "%s: dtype must be F32 or BF16",
+            w);
+    REQUIRE(rows >= 0 && rows <= INT32_MAX, CSA_ERR_INVALID_ARG, "%s: bad rows", w);
+    REQUIRE(d >= 16 && d <= 65536 && d % 16 == 0, CSA_ERR_UNSUPPORTED,
+            "%s: d = %d unsupported (a multiple of 16 from 16 to 65536)", w, d);
+    REQUIRE(!normalise || eps > 0.f, CSA_ERR_INVALID_ARG, "%s: eps must be positive", w);
+    REQUIRE(normalise || !gamma, CSA_ERR_INVALID_ARG, "%s: gamma needs normalise", w);
+    if (rows == 0)
+        return launched(cudaSuccess, w);
+    REQUIRE(x, CSA_ERR_INVALID_ARG, "%s: x is NULL", w);
+    REQUIRE(!codes == !scale, CSA_ERR_INVALID_ARG, "%s: codes and scale go together", w);
+    REQUIRE(total || y || codes, CSA_ERR_INVALID_ARG, "%s: no output is given", w);
+    REQUIRE(!total || residual, CSA_ERR_INVALID_ARG, "%s: total needs residual", w);
+    REQUIRE(aligned16(x) && aligned16(residual) && aligned16(total) && aligned16(y) &&
+                aligned16(codes),
+            CSA_ERR_INVALID_ARG, "%s: buffers must be 16-byte aligned", w);
+    REQUIRE(aligned4(gamma) && aligned4(scale), CSA_ERR_INVALID_ARG,
+            "%s: gamma and scale must be 4-byte aligned", w);
+    REQUIRE(!total || (total != y && total != codes), CSA_ERR_INVALID_ARG,
+            "%s: outputs must not overlap", w);
+    REQUIRE(!y || (y != codes && y != residual), CSA_ERR_INVALID_ARG, "%s: y overlaps", w);
+    REQUIRE(!codes || (codes != x && codes != residual), CSA_ERR_INVALID_ARG,
+            "%s: codes must not overlap an input", w);
+    csa::AddNormQuantArgs a{x, residual, gamma, dt, rows, d, normalise ? 1 : 0, eps, total, y,
+                            (uint8_t *)codes, scale};
+    return launched(csa::launch_add_norm_quant(a, (cudaStream_t)stream), w);
+}
+
+csa_status csa_quantize_weight(const void *W, csa_dtype dt, int64_t N, int K, void *codes,
+                               float *scale, void *stream)
+{
+    const char *w = "csa_quantize_weight";
+    REQUIRE(dt == CSA_F32 || dt == CSA_BF16, CSA_ERR_UNSUPPORTED, "%s: dtype must be F32 or BF16",
+            w);
+    REQUIRE(N >= 0 && N <= INT32_MAX, CSA_ERR_INVALID_ARG, "%s: bad N", w);
+    REQUIRE(K >= 16 && K % 16 == 0, CSA_ERR_UNSUPPORTED, "%s: K = %d must be a multiple of 16", w,
+            K);
+    if (N == 0)
+        return launched(cudaSuccess, w);
+    REQUIRE(W && codes && scale, CSA_ERR_INVALID_ARG, "%s: W, codes and scale are required", w);
+    REQUIRE(aligned16(W) && aligned16(codes) && aligned4(scale), CSA_ERR_INVALID_ARG,
+            "%s: W and codes must be 16-byte aligned", w);
+    REQUIRE(W != codes, CSA_ERR_INVALID_ARG, "%s: codes must not overlap W", w);
+    csa::QuantWeightArgs a{W, dt, N, K, (uint8_t *)codes, scale};
+    return launched(csa::launch_quantize_weight(a, (cudaStream_t)stream), w);
+}
+
+csa_status csa_fp8_proj(const void *A, const float *A_scale, const void *W, const float *W_scale,
+                        int64_t M, int N, int K, int groups, csa_dtype out_dt, void *out,
+                        float *out_scale, void *stream)
+{
+    const char *w = "csa_fp8_proj";
+    REQUIRE(out_dt == CSA_F32 || out_dt == CSA_BF16 || out_dt == CSA_E4M3, CSA_ERR_UNSUPPORTED,
+            "%s: output dtype must be F32, BF16 or E4M3", w);
+    REQUIRE(M >= 0 && M <= INT32_MAX && N >= 1 && groups >= 1, CSA_ERR_INVALID_ARG,
+            "%s: bad M / N / groups", w);
+    REQUIRE(K >= 16 && K % 16 == 0, CSA_ERR_UNSUPPORTED, "%s: K = %d must be a multiple of 16", w,
+            K);
+    REQUIRE((int64_t)groups * N <= INT32_MAX && (int64_t)groups * K <= INT32_MAX,
+            CSA_ERR_INVALID_ARG, "%s: groups N or groups K too large", w);
+    REQUIRE(groups == 1 || (N % 128 == 0 && K % 128 == 0), CSA_ERR_UNSUPPORTED,
+            "%s: several groups need N and K multiples of 128", w);
+    REQUIRE(out_dt != CSA_E4M3 || N % 16 == 0, CSA_ERR_UNSUPPORTED,
+            "%s: e4m3 output needs N a multiple of 16", w);
+    if (M == 0)
+        return launched(cudaSuccess, w);
+    REQUIRE(A && A_scale && W && W_scale && out, CSA_ERR_INVALID_ARG,
+            "%s: A, A_scale, W, W_scale and out are required", w);
+    REQUIRE((out_dt == CSA_E4M3) == (out_scale != nullptr), CSA_ERR_INVALID_ARG,
+            "%s: out_scale must be given exactly for e4m3 output", w);
+    REQUIRE(aligned16(A) && aligned16(W) && aligned16(out), CSA_ERR_INVALID_ARG,
+            "%s: A, W and out must be 16-byte aligned", w);
+    REQUIRE(aligned4(A_scale) && aligned4(W_scale) && aligned4(out_scale), CSA_ERR_INVALID_ARG,
+            "%s: scales must be 4-byte aligned", w);
+    REQUIRE(out != A && out != W && out != A_scale && out != W_scale, CSA_ERR_INVALID_ARG,
+            "%s: out must not overlap an operand", w);
+    unsigned *err = err_word();
+    REQUIRE(err, CSA_ERR_CUDA, "%s: no CUDA device", w);
+    csa::Fp8ProjArgs a{(const uint8_t *)A, A_scale, (const uint8_t *)W, W_scale, M, N, K, groups,
+                       out_dt, out, out_scale};
+    return launched(csa::launch_fp8_proj(a, err, (cudaStream_t)stream), w);
 }
 
 csa_status csa_debug_wait_probe(uint64_t limit_ns, void *stream)

@@ -162,6 +162,45 @@ struct GemmArgs {
 };
 cudaError_t launch_gemm_nt(const GemmArgs &g, unsigned *err, cudaStream_t s);
 
+// The 8-bit projections: s = x + residual, its RMSNorm and e4m3 storage
+// (csa_add_norm_quant); a weight's e4m3 storage in 128 x 128 blocks
+// (csa_quantize_weight); the block-scaled product (csa_fp8_proj).
+struct AddNormQuantArgs {
+    const void *x, *residual;
+    const float *gamma;
+    csa_dtype dt;
+    int64_t rows;
+    int d, normalise;
+    float eps;
+    void *total, *y;
+    uint8_t *codes;
+    float *scale;
+};
+cudaError_t launch_add_norm_quant(const AddNormQuantArgs &a, cudaStream_t s);
+
+struct QuantWeightArgs {
+    const void *W;
+    csa_dtype dt;
+    int64_t N;
+    int K;
+    uint8_t *codes;
+    float *scale;
+};
+cudaError_t launch_quantize_weight(const QuantWeightArgs &a, cudaStream_t s);
+
+struct Fp8ProjArgs {
+    const uint8_t *A;
+    const float *As;
+    const uint8_t *W;
+    const float *Ws;
+    int64_t M;
+    int N, K, groups;     // per group
+    csa_dtype out_dt;
+    void *out;
+    float *out_scale;
+};
+cudaError_t launch_fp8_proj(const Fp8ProjArgs &a, unsigned *err, cudaStream_t s);
+
 // One bounded wait that nothing completes (csa_debug_wait_probe).
 cudaError_t launch_wait_probe(uint64_t limit_ns, unsigned *err, cudaStream_t s);
 
