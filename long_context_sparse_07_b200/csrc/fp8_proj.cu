@@ -3,124 +3,655 @@
 //   r[t, j] = sum_b As[t, b] Ws[j / 128, b] sum_{k in block b} A[t, k] W[j, k],
 // blocks b of 128 inputs, float32 sums; bf16, float32 or e4m3 results.
 //
-// CUDA cores: a block of threads owns 32 tokens x 128 features, a warp four
-// of the tokens with all 128 features (so that an output scale's block lies in
-// one warp). Operands are decoded to float in shared memory 32 inputs at a
-// time; each block of 128 inputs is summed by itself, then scaled and added.
+// Both kernels feed the 5th-generation tensor cores (kind::f8f6f4) from a TMA
+// ring whose stages are one block of 128 inputs: the products of a block are
+// summed in tensor memory from zero, and the epilogue warps add the block's
+// sum, times its scale, to float32 registers while the next block's MMAs run
+// into another tensor-memory buffer. (The scales are arbitrary floats, one per
+// token and block, so they cannot ride in the MMA itself.)
+//
+// proj_rows_kernel (many tokens): tokens on the MMA's M axis, so that an
+// epilogue thread owns one token and multiplies a block's sums by one scale.
+// proj_cols_kernel (few tokens): features on the M axis and tokens on N, so
+// that one token costs a 16-wide MMA and not a 128-row one; the blocks of
+// inputs are split over a cluster of thread blocks, whose partial results are
+// added through distributed shared memory in the order of their ranks.
+//
+// Every wait is bounded; on expiry the kernel records CSA_ERR_TIMEOUT, lets
+// its copies and products land and returns.
 #include <float.h>
 
 #include "common.cuh"
 #include "kernels.h"
+#include "tc.cuh"
+#include "tma_host.h"
 
 namespace csa {
 
 namespace {
 
-constexpr int PM = 32, PN = 128, PK = 32, PB = 128;
-constexpr int PTHREADS = 256;
+constexpr int PB = 128;            // inputs per scale block = K of a ring stage
+constexpr int UK = 32;             // K of one 8-bit MMA
 
-__global__ void __launch_bounds__(PTHREADS)
-fp8_proj_kernel(const Fp8ProjArgs a)
+struct ProjDev {
+    const float *As, *Ws;
+    void *out;
+    float *out_scale;
+    unsigned *err;
+    int64_t M, ldo;                // ldo = groups N
+    int N, K, groups, nb, las, nbo;  // las = groups nb, nbo = ceil(ldo / 128)
+    csa_dtype out_dt;
+};
+
+// The e4m3 scale of a block of results whose largest magnitude has the bits m.
+__device__ __forceinline__ float out_block_scale(uint32_t m)
 {
-    __shared__ float sa[PK][PM + 4], sw[PK][PN + 4];
-    const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-    const int nb = (a.K + PB - 1) / PB, nt = (a.N + PN - 1) / PN;
-    const int64_t lda = (int64_t)a.groups * a.K, ldo = (int64_t)a.groups * a.N;
-    const int64_t m0 = (int64_t)(blockIdx.x / (nt * a.groups)) * PM;
-    const int g = blockIdx.x / nt % a.groups;
-    const int n0 = blockIdx.x % nt * PN;              // first feature, within the group
-    const uint8_t *A = a.A + (int64_t)g * a.K;
-    const uint8_t *W = a.W + (int64_t)g * a.N * a.K;
-    const float *As = a.As + (int64_t)g * nb;
-    const float *Ws = a.Ws + ((int64_t)g * a.N + n0) / PB * nb;
-    float acc[4][4] = {};
-    for (int b = 0; b < nb; b++) {
-        float p[4][4] = {};
-        for (int k0 = b * PB; k0 < min(a.K, (b + 1) * PB); k0 += PK) {
-            __syncthreads();
-            for (int i = threadIdx.x; i < (PM + PN) * PK / 4; i += PTHREADS) {
-                const int r = i / (PK / 4), k = i % (PK / 4) * 4;
-                const bool is_a = r < PM;
-                const int64_t row = is_a ? m0 + r : (int64_t)n0 + r - PM;
-                uint32_t u = 0;
-                if (row < (is_a ? a.M : (int64_t)a.N) && k0 + k < a.K)
-                    u = *(const uint32_t *)((is_a ? A + row * lda : W + row * a.K) + k0 + k);
-#pragma unroll
-                for (int e = 0; e < 4; e++) {
-                    const float v = e4m3_to_float((uint8_t)(u >> (8 * e)));
-                    if (is_a)
-                        sa[k + e][r] = v;
-                    else
-                        sw[k + e][r - PM] = v;
+    const float s = __uint_as_float(m) / 448.0f;
+    return s < FLT_MIN ? FLT_MIN : s;
+}
+
+__device__ __forceinline__ uint32_t mag_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+
+__device__ __forceinline__ uint32_t codes_4(float a, float b, float c, float d, float s)
+{
+    return float2_to_e4m3x2(a / s, b / s) | (uint32_t)float2_to_e4m3x2(c / s, d / s) << 16;
+}
+
+__device__ __forceinline__ uint32_t bf16_2(float a, float b)
+{
+    const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
+    return *(const uint32_t *)&p;
+}
+
+// ------------------------------------------------------------ many tokens
+
+// Tiles of 128 tokens x TN features. Warp 0 issues the TMA loads, warp 1 the
+// MMAs, TN / 32 epilogue warps each own a TMEM lane quarter (32 tokens) and
+// 128 features (one output scale's block). Tensor memory holds 512 / TN
+// accumulators of one block each.
+template <int TN> struct Rows {
+    static constexpr int STAGES = TN == 256 ? 4 : 6;
+    static constexpr int NBUF = 512 / TN;
+    static constexpr int EPI = TN / 32;
+    static constexpr int THREADS = 64 + 32 * EPI;
+    static constexpr uint32_t A_BYTES = 128 * PB, B_BYTES = TN * PB;
+    static constexpr size_t SMEM = 1024 + STAGES * (A_BYTES + B_BYTES) + 256;
+};
+
+template <int TN>
+__global__ void __launch_bounds__(Rows<TN>::THREADS, 1)
+proj_rows_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmW,
+                 const ProjDev a)
+{
+    using R = Rows<TN>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    uint8_t *sA = sm;
+    uint8_t *sB = sm + R::STAGES * R::A_BYTES;
+    uint64_t *full = (uint64_t *)(sB + R::STAGES * R::B_BYTES), *empty = full + R::STAGES;
+    uint64_t *accf = empty + R::STAGES, *acce = accf + R::NBUF, *done = acce + R::NBUF;
+    uint32_t *tmem_slot = (uint32_t *)(done + 1);
+    int *abort_flag = (int *)(tmem_slot + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t mt = (a.M + 127) / 128;
+    const int nt = (a.N + TN - 1) / TN;
+    const int64_t ntiles = (int64_t)a.groups * mt * nt;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < R::STAGES; i++) {
+            tc::mbar_init(&full[i], 1);
+            tc::mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < R::NBUF; i++) {
+            tc::mbar_init(&accf[i], 1);
+            tc::mbar_init(&acce[i], R::EPI);
+        }
+        tc::mbar_init(done, 1);
+        tc::fence_mbar_init();
+        *abort_flag = 0;
+        tc::tma_prefetch_desc(&tmA);
+        tc::tma_prefetch_desc(&tmW);
+    }
+    if (warp == 1) {
+        tc::tmem_alloc(tmem_slot, 512);
+        tc::tmem_relinquish();
+    }
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    const uint32_t tmem = *tmem_slot;
+    volatile int *abortv = abort_flag;
+
+    // tile t -> (group, m tile, n tile), n fastest: the blocks working at one
+    // time share their tokens through L2
+    auto coords = [&](int64_t t, int &grp, int64_t &mi, int &ni) {
+        ni = (int)(t % nt);
+        const int64_t r = t / nt;
+        mi = r % mt;
+        grp = (int)(r / mt);
+    };
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // ---------------- producer
+            uint32_t it = 0;
+            bool ok = true;
+            for (int64_t t = blockIdx.x; t < ntiles && ok; t += gridDim.x) {
+                int grp, ni;
+                int64_t mi;
+                coords(t, grp, mi, ni);
+                const int ax = grp * a.K, ay = (int)(mi * 128), wy = grp * a.N + ni * TN;
+                for (int b = 0; b < a.nb; b++, it++) {
+                    const int st = it % R::STAGES;
+                    if (it >= R::STAGES &&
+                        !tc::mbar_wait(&empty[st], ((it / R::STAGES) - 1) & 1, abortv)) {
+                        ok = false;
+                        break;
+                    }
+                    tc::mbar_arrive_expect_tx(&full[st], R::A_BYTES + R::B_BYTES);
+                    tc::tma_load_2d(sA + st * R::A_BYTES, &tmA, &full[st], ax + b * PB, ay);
+                    tc::tma_load_2d(sB + st * R::B_BYTES, &tmW, &full[st], b * PB, wy);
                 }
             }
-            __syncthreads();
-#pragma unroll 8
-            for (int k = 0; k < PK; k++) {
-                const float4 x = *(const float4 *)&sa[k][ty * 4];
-                const float4 w = *(const float4 *)&sw[k][tx * 4];
-                const float xv[4] = {x.x, x.y, x.z, x.w}, wv[4] = {w.x, w.y, w.z, w.w};
+            if (!ok) {
+                *abort_flag = 1;
+                report(a.err, CSA_ERR_TIMEOUT, K_FP8_PROJ, blockIdx.x, 0);
+            }
+            // let the copies in flight land before the block exits
+            volatile int never = 0;
+            for (uint32_t j = it > R::STAGES ? it - R::STAGES : 0; j < it; j++)
+                static_cast<void>(tc::mbar_wait(&full[j % R::STAGES], (j / R::STAGES) & 1, &never,
+                                                200000000ull));
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            // ---------------- MMA issuer
+            constexpr uint32_t idesc = tc::idesc_e4m3(128, TN);
+            uint32_t it = 0;
+            bool ok = true;
+            const uint32_t sAa = tc::smem_u32(sA), sBa = tc::smem_u32(sB);
+            for (int64_t t = blockIdx.x; t < ntiles && ok; t += gridDim.x) {
+                for (int b = 0; b < a.nb; b++, it++) {
+                    const int st = it % R::STAGES, buf = it % R::NBUF;
+                    if ((it >= R::NBUF &&
+                         !tc::mbar_wait(&acce[buf], ((it / R::NBUF) - 1) & 1, abortv)) ||
+                        !tc::mbar_wait(&full[st], (it / R::STAGES) & 1, abortv)) {
+                        ok = false;
+                        break;
+                    }
+                    tc::fence_after();
 #pragma unroll
-                for (int i = 0; i < 4; i++)
+                    for (int kk = 0; kk < PB / UK; kk++)
+                        tc::mma_f8(tmem + buf * TN,
+                                   tc::sdesc_sw128(sAa + st * R::A_BYTES + kk * UK),
+                                   tc::sdesc_sw128(sBa + st * R::B_BYTES + kk * UK), idesc, kk != 0);
+                    tc::mma_commit(&empty[st]);
+                    tc::mma_commit(&accf[buf]);
+                }
+            }
+            if (!ok) {
+                *abort_flag = 1;
+                report(a.err, CSA_ERR_TIMEOUT, K_FP8_PROJ, blockIdx.x, 1);
+            }
+            tc::mma_commit(done);
+            volatile int never = 0;
+            static_cast<void>(tc::mbar_wait(done, 0, &never, 200000000ull));
+        }
+    } else {
+        // ---------------- epilogue: lane quarter warp % 4 = 32 tokens, the
+        // features part * 128 .. + 127 of the tile
+        const int q4 = warp & 3, part = (warp - 2) >> 2;
+        const uint32_t lane_addr = tmem + ((uint32_t)(q4 * 32) << 16) + part * 128;
+        uint32_t it = 0;
+        bool ok = true;
+        for (int64_t t = blockIdx.x; t < ntiles && ok; t += gridDim.x) {
+            int grp, ni;
+            int64_t mi;
+            coords(t, grp, mi, ni);
+            const int64_t r = mi * 128 + q4 * 32 + lane;
+            const int n0 = ni * TN + part * 128;      // first feature, within the group
+            const bool live = r < a.M && n0 < a.N;
+            const int64_t fb = ((int64_t)grp * a.N + n0) / PB;   // its scale block
+            const float *as = a.As + (live ? r * a.las + (int64_t)grp * a.nb : 0);
+            const float *ws = a.Ws + (live ? fb * a.nb : 0);
+            float2 acc[64];
 #pragma unroll
-                    for (int j = 0; j < 4; j++)
-                        p[i][j] = fmaf(xv[i], wv[j], p[i][j]);
+            for (int j = 0; j < 64; j++)
+                acc[j] = make_float2(0.f, 0.f);
+            float s = live ? as[0] * ws[0] : 0.f;
+            for (int b = 0; b < a.nb; b++, it++) {
+                const int buf = it % R::NBUF;
+                const float s_next = live && b + 1 < a.nb ? as[b + 1] * ws[b + 1] : 0.f;
+                if (!tc::mbar_wait(&accf[buf], (it / R::NBUF) & 1, abortv)) {
+                    *abort_flag = 1;
+                    report(a.err, CSA_ERR_TIMEOUT, K_FP8_PROJ, blockIdx.x, 2);
+                    ok = false;
+                    break;
+                }
+                tc::fence_after();
+                uint32_t v[2][16];
+                const float2 s2 = make_float2(s, s);
+                tc::tmem_ld16(lane_addr + buf * TN, v[0]);
+#pragma unroll
+                for (int c = 0; c < 8; c++) {
+                    tc::tmem_ld_wait(v[c & 1]);
+                    if (c < 7) {
+                        tc::tmem_ld16(lane_addr + buf * TN + (c + 1) * 16, v[(c + 1) & 1]);
+                    } else {
+                        tc::fence_before();
+                        __syncwarp();
+                        if (lane == 0)
+                            tc::mbar_arrive(&acce[buf]);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 8; j++)
+                        acc[c * 8 + j] =
+                            __ffma2_rn(make_float2(__uint_as_float(v[c & 1][2 * j]),
+                                                   __uint_as_float(v[c & 1][2 * j + 1])),
+                                       s2, acc[c * 8 + j]);
+                }
+                s = s_next;
+            }
+            if (!ok || !live)
+                continue;
+            const int64_t o = r * a.ldo + (int64_t)grp * a.N + n0;
+            const int cols = min(128, a.N - n0);
+            if (a.out_dt == CSA_BF16) {
+                __nv_bfloat16 *dst = (__nv_bfloat16 *)a.out + o;
+                if (cols == 128 && a.ldo % 8 == 0) {
+#pragma unroll
+                    for (int j = 0; j < 16; j++)
+                        ((uint4 *)dst)[j] =
+                            make_uint4(bf16_2(acc[4 * j].x, acc[4 * j].y),
+                                       bf16_2(acc[4 * j + 1].x, acc[4 * j + 1].y),
+                                       bf16_2(acc[4 * j + 2].x, acc[4 * j + 2].y),
+                                       bf16_2(acc[4 * j + 3].x, acc[4 * j + 3].y));
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 128; j++)
+                        if (j < cols)
+                            dst[j] = __float2bfloat16_rn(j & 1 ? acc[j / 2].y : acc[j / 2].x);
+                }
+            } else if (a.out_dt == CSA_F32) {
+                float *dst = (float *)a.out + o;
+                if (cols == 128 && a.ldo % 4 == 0) {
+#pragma unroll
+                    for (int j = 0; j < 32; j++)
+                        ((float4 *)dst)[j] = make_float4(acc[2 * j].x, acc[2 * j].y,
+                                                         acc[2 * j + 1].x, acc[2 * j + 1].y);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 128; j++)
+                        if (j < cols)
+                            dst[j] = j & 1 ? acc[j / 2].y : acc[j / 2].x;
+                }
+            } else {
+                uint32_t m = 0;                        // features behind the last are zero
+#pragma unroll
+                for (int j = 0; j < 64; j++)
+                    m = max(m, max(mag_bits(acc[j].x), mag_bits(acc[j].y)));
+                const float sc = out_block_scale(m);
+                a.out_scale[r * a.nbo + fb] = sc;
+                uint4 *dst = (uint4 *)((uint8_t *)a.out + o);
+#pragma unroll
+                for (int j = 0; j < 8; j++) {          // N is a multiple of 16
+                    uint32_t w[4];
+#pragma unroll
+                    for (int e = 0; e < 4; e++)
+                        w[e] = codes_4(acc[8 * j + 2 * e].x, acc[8 * j + 2 * e].y,
+                                       acc[8 * j + 2 * e + 1].x, acc[8 * j + 2 * e + 1].y, sc);
+                    if (16 * j < cols)
+                        dst[j] = make_uint4(w[0], w[1], w[2], w[3]);
+                }
             }
         }
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-            const int64_t t = m0 + ty * 4 + i;
-            const float s = t < a.M ? As[t * a.groups * nb + b] * Ws[b] : 0.f;
-#pragma unroll
-            for (int j = 0; j < 4; j++)
-                acc[i][j] = fmaf(p[i][j], s, acc[i][j]);
-        }
     }
+    tc::fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc::fence_after();
+        tc::tmem_dealloc(tmem, 512);
+    }
+}
+
+// ------------------------------------------------------------ few tokens
+
+// Tiles of 128 features x TT tokens, the blocks of inputs split over the
+// cluster's thread blocks. Warps as above, with four epilogue warps (a lane
+// quarter = 32 features each); an epilogue thread owns one feature and all TT
+// tokens. In the end a warp takes one token at a time and adds the cluster's
+// partial results of its 128 features.
+template <int TT> struct Cols {
+    static constexpr int STAGES = TT == 16 ? 5 : TT == 32 ? 5 : TT == 64 ? 4 : 6;
+    static constexpr int NBUF = TT == 128 ? 2 : 4;
+    static constexpr int THREADS = 192;
+    static constexpr uint32_t W_BYTES = 128 * PB, T_BYTES = TT * PB;
+    static constexpr uint32_t TMEM = NBUF * TT;
+    static constexpr size_t RING = STAGES * (W_BYTES + T_BYTES);
+    static constexpr size_t SMEM = 1024 + RING + 4 * 2 * TT * 4 + 256;
+    static_assert(RING >= (size_t)TT * 128 * 4, "partial results reuse the ring");
+};
+
+template <int TT>
+__global__ void __launch_bounds__(Cols<TT>::THREADS)
+proj_cols_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmW,
+                 const ProjDev a, const int split)
+{
+    using C = Cols<TT>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    uint8_t *sW = sm;
+    uint8_t *sT = sm + C::STAGES * C::W_BYTES;
+    float *sc = (float *)(sm + C::RING);              // [epilogue warp][2][TT]
+    uint64_t *full = (uint64_t *)(sc + 4 * 2 * TT), *empty = full + C::STAGES;
+    uint64_t *accf = empty + C::STAGES, *acce = accf + C::NBUF, *done = acce + C::NBUF;
+    uint32_t *tmem_slot = (uint32_t *)(done + 1);
+    int *abort_flag = (int *)(tmem_slot + 1);
+    float *partial = (float *)sm;                     // [TT][128], once the ring is drained
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = split > 1 ? (int)tc::cluster_rank() : 0;
+    const int64_t tile = blockIdx.x / split;
+    const int ft = (a.N + 127) / 128;
+    const int64_t tt = (a.M + TT - 1) / TT;
+    const int n0 = (int)(tile % ft) * 128;            // first feature, within the group
+    const int64_t t0 = tile / ft % tt * TT;           // first token
+    const int grp = (int)(tile / ft / tt);
+    const int b0 = (int)((int64_t)a.nb * rank / split);
+    const int b1 = (int)((int64_t)a.nb * (rank + 1) / split);
+    const uint32_t nblk = (uint32_t)(b1 - b0);
+    const int64_t fb = ((int64_t)grp * a.N + n0) / PB;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::STAGES; i++) {
+            tc::mbar_init(&full[i], 1);
+            tc::mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < C::NBUF; i++) {
+            tc::mbar_init(&accf[i], 1);
+            tc::mbar_init(&acce[i], 4);
+        }
+        tc::mbar_init(done, 1);
+        tc::fence_mbar_init();
+        *abort_flag = 0;
+    }
+    if (warp == 1) {
+        tc::tmem_alloc(tmem_slot, C::TMEM);
+        tc::tmem_relinquish();
+    }
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    const uint32_t tmem = *tmem_slot;
+    volatile int *abortv = abort_flag;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // ---------------- producer
+            uint32_t it = 0;
+            for (; it < nblk; it++) {
+                const int st = it % C::STAGES;
+                if (it >= C::STAGES &&
+                    !tc::mbar_wait(&empty[st], ((it / C::STAGES) - 1) & 1, abortv)) {
+                    *abort_flag = 1;
+                    report(a.err, CSA_ERR_TIMEOUT, K_FP8_PROJ, blockIdx.x, 3);
+                    break;
+                }
+                const int x = (b0 + (int)it) * PB;
+                tc::mbar_arrive_expect_tx(&full[st], C::W_BYTES + C::T_BYTES);
+                tc::tma_load_2d(sW + st * C::W_BYTES, &tmW, &full[st], x, grp * a.N + n0);
+                tc::tma_load_2d(sT + st * C::T_BYTES, &tmA, &full[st], grp * a.K + x, (int)t0);
+            }
+            volatile int never = 0;
+            for (uint32_t j = it > C::STAGES ? it - C::STAGES : 0; j < it; j++)
+                static_cast<void>(tc::mbar_wait(&full[j % C::STAGES], (j / C::STAGES) & 1, &never,
+                                                200000000ull));
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            // ---------------- MMA issuer
+            constexpr uint32_t idesc = tc::idesc_e4m3(128, TT);
+            const uint32_t sWa = tc::smem_u32(sW), sTa = tc::smem_u32(sT);
+            for (uint32_t it = 0; it < nblk; it++) {
+                const int st = it % C::STAGES, buf = it % C::NBUF;
+                if ((it >= C::NBUF &&
+                     !tc::mbar_wait(&acce[buf], ((it / C::NBUF) - 1) & 1, abortv)) ||
+                    !tc::mbar_wait(&full[st], (it / C::STAGES) & 1, abortv)) {
+                    *abort_flag = 1;
+                    report(a.err, CSA_ERR_TIMEOUT, K_FP8_PROJ, blockIdx.x, 4);
+                    break;
+                }
+                tc::fence_after();
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-        const int64_t t = m0 + ty * 4 + i;
-        const int64_t o = t * ldo + (int64_t)g * a.N + n0 + tx * 4;
-        float s = 1.f;
+                for (int kk = 0; kk < PB / UK; kk++)
+                    tc::mma_f8(tmem + buf * TT, tc::sdesc_sw128(sWa + st * C::W_BYTES + kk * UK),
+                               tc::sdesc_sw128(sTa + st * C::T_BYTES + kk * UK), idesc, kk != 0);
+                tc::mma_commit(&empty[st]);
+                tc::mma_commit(&accf[buf]);
+            }
+            tc::mma_commit(done);
+            volatile int never = 0;
+            static_cast<void>(tc::mbar_wait(done, 0, &never, 200000000ull));
+        }
+    } else {
+        // ---------------- epilogue: feature n0 + 32 (warp % 4) + lane
+        constexpr int CH = TT < 32 ? TT : 32;          // columns per load
+        constexpr int NS = (TT + 31) / 32;             // scales a lane brings
+        const int q4 = warp & 3;
+        const uint32_t lane_addr = tmem + ((uint32_t)(q4 * 32) << 16);
+        float *mine = sc + (warp - 2) * 2 * TT;
+        const float *ws = a.Ws + fb * a.nb;
+        auto scale_of = [&](int i, uint32_t it) {
+            const int64_t t = t0 + i * 32 + lane;
+            return it < nblk && t < a.M && i * 32 + lane < TT
+                       ? a.As[t * a.las + (int64_t)grp * a.nb + b0 + it] * ws[b0 + it]
+                       : 0.f;
+        };
+        float acc[TT], nxt[NS];
+#pragma unroll
+        for (int j = 0; j < TT; j++)
+            acc[j] = 0.f;
+#pragma unroll
+        for (int i = 0; i < NS; i++)
+            nxt[i] = scale_of(i, 0);
+        for (uint32_t it = 0; it < nblk; it++) {
+            const int buf = it % C::NBUF;
+            float *cur = mine + (it & 1) * TT;
+#pragma unroll
+            for (int i = 0; i < NS; i++) {
+                if (TT >= 32 || lane < TT)
+                    cur[i * 32 + lane] = nxt[i];
+                nxt[i] = scale_of(i, it + 1);
+            }
+            __syncwarp();
+            if (!tc::mbar_wait(&accf[buf], (it / C::NBUF) & 1, abortv)) {
+                *abort_flag = 1;
+                report(a.err, CSA_ERR_TIMEOUT, K_FP8_PROJ, blockIdx.x, 5);
+                break;
+            }
+            tc::fence_after();
+#pragma unroll
+            for (int c = 0; c < TT / CH; c++) {
+                uint32_t v[CH];
+                if constexpr (CH == 32)
+                    tc::tmem_ld32(lane_addr + buf * TT + c * CH, v);
+                else
+                    tc::tmem_ld16(lane_addr + buf * TT + c * CH, v);
+                tc::tmem_ld_wait(v);
+#pragma unroll
+                for (int j = 0; j < CH; j += 4) {
+                    const float4 s = *(const float4 *)&cur[c * CH + j];
+                    acc[c * CH + j] = fmaf(__uint_as_float(v[j]), s.x, acc[c * CH + j]);
+                    acc[c * CH + j + 1] = fmaf(__uint_as_float(v[j + 1]), s.y, acc[c * CH + j + 1]);
+                    acc[c * CH + j + 2] = fmaf(__uint_as_float(v[j + 2]), s.z, acc[c * CH + j + 2]);
+                    acc[c * CH + j + 3] = fmaf(__uint_as_float(v[j + 3]), s.w, acc[c * CH + j + 3]);
+                }
+            }
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0)
+                tc::mbar_arrive(&acce[buf]);
+        }
+        // the last accumulator's commit covers every MMA: the ring is drained
+#pragma unroll
+        for (int j = 0; j < TT; j++)
+            partial[j * 128 + q4 * 32 + lane] = acc[j];
+    }
+    tc::fence_before();
+    __syncthreads();
+    if (split > 1)
+        tc::cluster_sync();
+    // token t0 + j, features n0 + 4 lane .. + 3
+    const int nw = C::THREADS / 32;
+    for (int j = rank + split * warp; j < TT && t0 + j < a.M; j += split * nw) {
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int p = 0; p < split; p++) {
+            const float *src = partial + j * 128 + lane * 4;
+            const float4 u = split > 1 ? tc::cluster_ld4(src, p) : *(const float4 *)src;
+            v.x += u.x;
+            v.y += u.y;
+            v.z += u.z;
+            v.w += u.w;
+        }
+        const int cols = a.N - n0 - lane * 4;         // features of this lane that exist
+        const int64_t t = t0 + j, o = t * a.ldo + (int64_t)grp * a.N + n0 + lane * 4;
         if (a.out_dt == CSA_E4M3) {
-            uint32_t m = 0;                           // features behind the last one are zero
-#pragma unroll
-            for (int j = 0; j < 4; j++)
-                m = max(m, __float_as_uint(acc[i][j]) & 0x7fffffffu);
+            uint32_t m = max(max(mag_bits(v.x), mag_bits(v.y)), max(mag_bits(v.z), mag_bits(v.w)));
 #pragma unroll
             for (int f = 16; f > 0; f >>= 1)
                 m = max(m, __shfl_xor_sync(0xffffffffu, m, f));
-            s = __uint_as_float(m) / 448.0f;
-            if (s < FLT_MIN)
-                s = FLT_MIN;
-            if (tx == 0 && t < a.M)
-                a.out_scale[t * ((ldo + PB - 1) / PB) + ((int64_t)g * a.N + n0) / PB] = s;
-        }
-        if (t >= a.M)
-            continue;
+            const float s = out_block_scale(m);
+            if (lane == 0)
+                a.out_scale[t * a.nbo + fb] = s;
+            if (cols > 0)                              // N is a multiple of 16
+                *(uint32_t *)((uint8_t *)a.out + o) = codes_4(v.x, v.y, v.z, v.w, s);
+        } else if (a.ldo % 4 == 0) {
+            if (cols > 0) {
+                if (a.out_dt == CSA_BF16)
+                    *(uint2 *)((__nv_bfloat16 *)a.out + o) =
+                        make_uint2(bf16_2(v.x, v.y), bf16_2(v.z, v.w));
+                else
+                    *(float4 *)((float *)a.out + o) = v;
+            }
+        } else {
+            const float e[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int j = 0; j < 4; j++) {
-            if (n0 + tx * 4 + j >= a.N)
-                break;
-            if (a.out_dt == CSA_F32)
-                ((float *)a.out)[o + j] = acc[i][j];
-            else if (a.out_dt == CSA_BF16)
-                ((__nv_bfloat16 *)a.out)[o + j] = __float2bfloat16_rn(acc[i][j]);
-            else
-                ((uint8_t *)a.out)[o + j] = (uint8_t)float2_to_e4m3x2(acc[i][j] / s, 0.f);
+            for (int i = 0; i < 4; i++) {
+                if (i < cols) {
+                    if (a.out_dt == CSA_BF16)
+                        ((__nv_bfloat16 *)a.out)[o + i] = __float2bfloat16_rn(e[i]);
+                    else
+                        ((float *)a.out)[o + i] = e[i];
+                }
+            }
         }
     }
+    // no block leaves while another may still read its shared memory
+    if (split > 1) {
+        __syncwarp();
+        tc::cluster_sync();
+    }
+    if (warp == 1) {
+        tc::fence_after();
+        tc::tmem_dealloc(tmem, C::TMEM);
+    }
+}
+
+// ------------------------------------------------------------ launches
+
+int sm_count()
+{
+    int dev = 0, sms = 148;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    return sms;
+}
+
+template <int TN>
+cudaError_t launch_rows(const Fp8ProjArgs &g, const ProjDev &d, int sms, cudaStream_t s)
+{
+    using R = Rows<TN>;
+    CUtensorMap tmA, tmW;
+    if (!make_tmap_2d(&tmA, g.A, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)g.M,
+                      (uint64_t)g.groups * g.K, 128) ||
+        !make_tmap_2d(&tmW, g.W, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)d.ldo, (uint64_t)g.K,
+                      TN))
+        return cudaErrorInvalidValue;
+    cudaError_t e = cudaFuncSetAttribute(proj_rows_kernel<TN>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)R::SMEM);
+    if (e != cudaSuccess)
+        return e;
+    const int64_t tiles = (g.M + 127) / 128 * ((g.N + TN - 1) / TN) * g.groups;
+    proj_rows_kernel<TN><<<(unsigned)(tiles < sms ? tiles : sms), R::THREADS, R::SMEM, s>>>(
+        tmA, tmW, d);
+    return cudaGetLastError();
+}
+
+template <int TT>
+cudaError_t launch_cols(const Fp8ProjArgs &g, const ProjDev &d, int sms, cudaStream_t s)
+{
+    using C = Cols<TT>;
+    CUtensorMap tmA, tmW;
+    if (!make_tmap_2d(&tmA, g.A, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)g.M,
+                      (uint64_t)g.groups * g.K, TT) ||
+        !make_tmap_2d(&tmW, g.W, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)d.ldo, (uint64_t)g.K,
+                      128))
+        return cudaErrorInvalidValue;
+    cudaError_t e = cudaFuncSetAttribute(proj_cols_kernel<TT>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
+    if (e != cudaSuccess)
+        return e;
+    const int64_t tiles = (g.M + TT - 1) / TT * ((g.N + 127) / 128) * g.groups;
+    int split = 1;
+    while (split < 8 && tiles * split * 2 <= sms && split * 2 <= d.nb)
+        split *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(tiles * split));
+    cfg.blockDim = dim3(C::THREADS);
+    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim = {(unsigned)split, 1, 1};
+    cfg.attrs = at;
+    cfg.numAttrs = split > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, proj_cols_kernel<TT>, tmA, tmW, d, split);
 }
 
 }  // namespace
 
-cudaError_t launch_fp8_proj(const Fp8ProjArgs &a, unsigned *err, cudaStream_t s)
+cudaError_t launch_fp8_proj(const Fp8ProjArgs &g, unsigned *err, cudaStream_t s)
 {
-    (void)err;
-    const int64_t tiles = (a.M + PM - 1) / PM * ((a.N + PN - 1) / PN) * a.groups;
-    if (tiles > INT32_MAX)
-        return cudaErrorInvalidConfiguration;
-    fp8_proj_kernel<<<(unsigned)tiles, PTHREADS, 0, s>>>(a);
-    return cudaGetLastError();
+    ProjDev d;
+    d.As = g.As;
+    d.Ws = g.Ws;
+    d.out = g.out;
+    d.out_scale = g.out_scale;
+    d.err = err;
+    d.M = g.M;
+    d.ldo = (int64_t)g.groups * g.N;
+    d.N = g.N;
+    d.K = g.K;
+    d.groups = g.groups;
+    d.nb = (g.K + PB - 1) / PB;
+    d.las = g.groups * d.nb;
+    d.nbo = (int)((d.ldo + PB - 1) / PB);
+    d.out_dt = g.out_dt;
+    const int sms = sm_count();
+    // 128 x 128 tiles that the call has
+    const int64_t tiles = (g.M + 127) / 128 * ((g.N + 127) / 128) * g.groups;
+    if (g.M <= 16)
+        return launch_cols<16>(g, d, sms, s);
+    if (g.M <= 32)
+        return launch_cols<32>(g, d, sms, s);
+    if (g.M <= 64)
+        return launch_cols<64>(g, d, sms, s);
+    if (2 * tiles <= sms)
+        return launch_cols<128>(g, d, sms, s);
+    if (tiles <= 2 * sms)
+        return launch_rows<128>(g, d, sms, s);
+    return launch_rows<256>(g, d, sms, s);
 }
 
 }  // namespace csa
