@@ -6,7 +6,11 @@
 //   s = x + residual,  v = s / sqrt(mean_j s_j^2 + eps) * gamma,
 //   a_b = max(max_{j in b} |v_j| / 448, 2^-126) per block b of 128 channels,
 //   code_j = e4m3(v_j / a_b), rounded to nearest even.
-// Both kernels stream: HBM bytes bound them.
+// HBM bytes bound these kernels as long as a value costs few instructions: at
+// 3 bytes a value (unnormed bf16) an SM has about 16 issue slots for each.
+// Hence packed pairs of float32 (one instruction for two values), quotients
+// without a division, and 16 consecutive values to a lane, so that a scale's
+// block is 8 lanes and its maximum three shuffles for every 16 values.
 #include <float.h>
 
 #include "common.cuh"
@@ -18,167 +22,143 @@ namespace {
 
 constexpr int kBlock = 128;       // values that share a scale (along a row)
 constexpr int kThreads = 256;
+constexpr int kLane = 16;         // consecutive values of a lane
+constexpr int kPairs = kLane / 2;
 
-// 8 consecutive values, as float.
-__device__ __forceinline__ void load_8(const __nv_bfloat16 *p, float *v) { load8(p, v); }
-__device__ __forceinline__ void load_8(const float *p, float *v)
-{
-    load4(p, v);
-    load4(p + 4, v + 4);
-}
-
-__device__ __forceinline__ void store_8(__nv_bfloat16 *p, const float *v)
-{
-    uint4 u;
-    __nv_bfloat162 *h = reinterpret_cast<__nv_bfloat162 *>(&u);
-#pragma unroll
-    for (int i = 0; i < 4; i++)
-        h[i] = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-    *reinterpret_cast<uint4 *>(p) = u;
-}
-__device__ __forceinline__ void store_8(float *p, const float *v)
-{
-    reinterpret_cast<float4 *>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-    reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
-}
-
-// Magnitude as an unsigned integer: ordered like the magnitude, a NaN above all.
-__device__ __forceinline__ uint32_t mag(float v) { return __float_as_uint(v) & 0x7fffffffu; }
-
-// Scale of a block whose largest magnitude has the bits m (a NaN stays one).
-__device__ __forceinline__ float block_scale(uint32_t m)
-{
-    const float s = __uint_as_float(m) / 448.0f;
-    return s < FLT_MIN ? FLT_MIN : s;
-}
-
-// Quotients by one block's scale, each the correctly rounded float32 v / s.
-// Between 2^-100 and 2^100 (where no step below under- or overflows) as
-// Markstein's theorem gives it: with r the rounded reciprocal and q = v r,
-// q + r (v - q s) rounds to the rounded quotient (P. Markstein, "Computation
-// of elementary functions on the IBM RISC System/6000 processor", 1990); three
-// FMA-pipe instructions a value, where a division each left the weight's
-// kernel bound by arithmetic. Other scales (NaN among them) divide.
-struct Quotient {
-    float s, r;
-    bool fast;
-    __device__ __forceinline__ explicit Quotient(float scale)
-        : s(scale), r(1.f / scale), fast(scale >= 0x1p-100f && scale <= 0x1p100f) {}
-    __device__ __forceinline__ float quick(float v) const
-    {
-        const float q = v * r;
-        return fmaf(fmaf(-q, s, v), r, q);
-    }
-};
-
-__device__ __forceinline__ uint2 codes_8(const float *v, const Quotient &q)
-{
-    uint16_t c[4];
-    if (q.fast) {
-#pragma unroll
-        for (int i = 0; i < 4; i++)
-            c[i] = float2_to_e4m3x2(q.quick(v[2 * i]), q.quick(v[2 * i + 1]));
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; i++)
-            c[i] = float2_to_e4m3x2(v[2 * i] / q.s, v[2 * i + 1] / q.s);
-    }
-    return make_uint2(c[0] | (uint32_t)c[1] << 16, c[2] | (uint32_t)c[3] << 16);
-}
-
-// 16 bytes that are read once: past L1.
-__device__ __forceinline__ uint4 load_once(const void *p) { return __ldcs((const uint4 *)p); }
-
-// 8 consecutive values as they lie in memory.
-template <typename T> struct Raw8 {
-    uint4 u[sizeof(T) / 2];
+// 16 consecutive values as they lie in memory.
+template <typename T> struct Raw {
+    uint4 u[sizeof(T)];
     __device__ __forceinline__ void load(const T *p)
     {
 #pragma unroll
-        for (int i = 0; i < (int)sizeof(T) / 2; i++)
-            u[i] = load_once((const uint4 *)p + i);
+        for (int i = 0; i < (int)sizeof(T); i++)
+            u[i] = ((const uint4 *)p)[i];
     }
-    __device__ __forceinline__ void floats(float *v) const
+    __device__ __forceinline__ float2 pair(int i) const
     {
         const uint32_t *w = (const uint32_t *)u;
-#pragma unroll
-        for (int e = 0; e < 8; e++)
-            v[e] = sizeof(T) == 4 ? __uint_as_float(w[e])
-                                  : __uint_as_float(e & 1 ? w[e / 2] & 0xffff0000u : w[e / 2] << 16);
+        if (sizeof(T) == 4)
+            return make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+        return make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
     }
 };
 
-// Largest magnitude of a scale's block: the 16 lanes of a half warp.
-__device__ __forceinline__ uint32_t half_warp_max(uint32_t m)
+__device__ __forceinline__ void store_16(__nv_bfloat16 *p, const float2 (&v)[kPairs])
 {
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1)
-        m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    for (int i = 0; i < 2; i++) {
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+            const __nv_bfloat162 h = __float22bfloat162_rn(v[4 * i + e]);
+            w[e] = *(const uint32_t *)&h;
+        }
+        ((uint4 *)p)[i] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+__device__ __forceinline__ void store_16(float *p, const float2 (&v)[kPairs])
+{
+#pragma unroll
+    for (int i = 0; i < 4; i++)
+        ((float4 *)p)[i] = make_float4(v[2 * i].x, v[2 * i].y, v[2 * i + 1].x, v[2 * i + 1].y);
+}
+
+// Largest of m and two magnitudes; a NaN wins.
+__device__ __forceinline__ float max_mag(float m, float2 v)
+{
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(m), "f"(v.x), "f"(v.y));
     return m;
 }
 
-// s of CH chunks of 8 values (chunk i at j + i * step), all loads in flight
-// together; zeros behind the row's end.
-template <typename T, int CH>
-__device__ __forceinline__ void load_sums(const T *x, const T *residual, int64_t base, int d,
-                                          int j, int step, float (&v)[CH][8])
+__device__ __forceinline__ float max_nan(float a, float b)
 {
-    Raw8<T> a[CH], b[CH];
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(a) : "f"(a), "f"(b));
+    return a;
+}
+
+// Largest magnitude of a scale's block: 16 values of each of 8 lanes.
+__device__ __forceinline__ float block_max(const float2 (&v)[kPairs], float m = 0.f)
+{
 #pragma unroll
-    for (int i = 0; i < CH; i++)
-        if (j + i * step < d)
-            a[i].load(x + base + j + i * step);
-    if (residual) {
+    for (int i = 0; i < kPairs; i++)
+        m = max_mag(m, v[i]);
+    return m;
+}
+
+__device__ __forceinline__ float eight_lane_max(float m)
+{
 #pragma unroll
-        for (int i = 0; i < CH; i++)
-            if (j + i * step < d)
-                b[i].load(residual + base + j + i * step);
-    }
+    for (int o = 4; o > 0; o >>= 1)
+        m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+    return m;
+}
+
+// Scale of a block with the largest magnitude m (a NaN stays one).
+__device__ __forceinline__ float block_scale(float m)
+{
+    const float s = m / 448.0f;
+    return s < FLT_MIN ? FLT_MIN : s;
+}
+
+__device__ __forceinline__ uint16_t codes_2(float2 q)
+{
+    return (uint16_t)__nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3);
+}
+
+// Codes of 16 values of a block with scale s, each from the correctly rounded
+// float32 quotient v / s. Between 2^-100 and 2^100 (where no step below under-
+// or overflows) the quotient is taken as Markstein's theorem gives it: with r
+// the rounded reciprocal and q = v r, q + r (v - q s) rounds to the rounded
+// quotient (P. Markstein, "Computation of elementary functions on the IBM RISC
+// System/6000 processor", 1990): three packed instructions for two values.
+// Other scales (NaN among them) divide.
+__device__ __forceinline__ uint4 codes_16(const float2 (&v)[kPairs], float s)
+{
+    uint32_t w[4];
+    if (s >= 0x1p-100f && s <= 0x1p100f) {
+        const float r = 1.f / s;
+        const float2 r2 = make_float2(r, r), s2 = make_float2(-s, -s);
 #pragma unroll
-    for (int i = 0; i < CH; i++) {
-        if (j + i * step < d) {
-            a[i].floats(v[i]);
-            if (residual) {
-                float r[8];
-                b[i].floats(r);
+        for (int i = 0; i < 4; i++) {
+            uint32_t h[2];
 #pragma unroll
-                for (int e = 0; e < 8; e++)
-                    v[i][e] += r[e];
+            for (int e = 0; e < 2; e++) {
+                const float2 x = v[2 * i + e], q = __fmul2_rn(x, r2);
+                h[e] = codes_2(__ffma2_rn(__ffma2_rn(q, s2, x), r2, q));
             }
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; e++)
-                v[i][e] = 0.f;
+            w[i] = h[0] | h[1] << 16;
         }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+            w[i] = codes_2(make_float2(v[2 * i].x / s, v[2 * i].y / s)) |
+                   (uint32_t)codes_2(make_float2(v[2 * i + 1].x / s, v[2 * i + 1].y / s)) << 16;
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// The 16 gains from gamma + j: only 4-byte aligned in general.
+__device__ __forceinline__ void load_gains(const float *gamma, int j, bool aligned,
+                                           float2 (&g)[kPairs])
+{
+    if (aligned) {
+#pragma unroll
+        for (int e = 0; e < kPairs; e += 2) {
+            const float4 f = __ldg((const float4 *)(gamma + j + 2 * e));
+            g[e] = make_float2(f.x, f.y);
+            g[e + 1] = make_float2(f.z, f.w);
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < kPairs; e++)
+            g[e] = make_float2(__ldg(gamma + j + 2 * e), __ldg(gamma + j + 2 * e + 1));
     }
 }
 
-// Rows of up to 8 CH tpr values, tpr threads (a multiple of 32) to a row and
-// blockDim / tpr rows to a block. A thread holds CH chunks of 8 values, tpr
-// chunks apart, from the one read to the outputs (HOLD), so that each byte
-// crosses HBM once and only the sum of squares is exchanged; 16 lanes hold a
-// scale's block. Rows too long for the registers are read a second time.
-template <typename T, int CH, bool HOLD>
-__global__ void __launch_bounds__(HOLD ? 512 : 1024)
-add_norm_quant_kernel(const T *x, const T *residual, const float *__restrict__ gamma, int64_t rows,
-                      int d, int tpr, float eps, T *total, T *y, uint8_t *codes, float *scale)
+// Sum over a row's tpr threads (a multiple of 32); `part` is this call's own
+// place of 32 floats. Threads of other rows of the block take part as well.
+__device__ __forceinline__ float row_sum(float ss, int tpr, int sub, float *part)
 {
-    __shared__ float part[32];
-    const int sub = threadIdx.x % tpr;
-    const int64_t row = (int64_t)blockIdx.x * (blockDim.x / tpr) + threadIdx.x / tpr;
-    const int64_t base = row * d;
-    const int nb = (d + kBlock - 1) / kBlock;
-    const int dl = row < rows ? d : 0;                // nothing of rows behind the last
-    float v[CH][8];
-    float ss = 0.f;
-    for (int j0 = 0; j0 < (HOLD ? 1 : d); j0 += CH * tpr * 8) {
-        load_sums<T, CH>(x, residual, base, dl, j0 + sub * 8, tpr * 8, v);
-#pragma unroll
-        for (int i = 0; i < CH; i++)
-#pragma unroll
-            for (int e = 0; e < 8; e++)
-                ss = fmaf(v[i][e], v[i][e], ss);
-    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
         ss += __shfl_xor_sync(0xffffffffu, ss, o);
@@ -191,178 +171,310 @@ add_norm_quant_kernel(const T *x, const T *residual, const float *__restrict__ g
         for (int i = 0; i < tpr / 32; i++)
             ss += part[w0 + i];
     }
-    const float inv = 1.f / sqrtf(ss / d + eps);
-    for (int j0 = 0; j0 < (HOLD ? 1 : d); j0 += CH * tpr * 8) {
-        if (!HOLD)
-            load_sums<T, CH>(x, residual, base, dl, j0 + sub * 8, tpr * 8, v);
-#pragma unroll
-        for (int i = 0; i < CH; i++) {
-            const int j = j0 + (i * tpr + sub) * 8;
-            const bool live = j < dl;
-            uint32_t m = 0;
-            if (live) {
-                if (total)
-                    store_8(total + base + j, v[i]);
-                float g[8];
-                if (gamma)
-                    load_8(gamma + j, g);
-#pragma unroll
-                for (int e = 0; e < 8; e++)
-                    v[i][e] = v[i][e] * inv * (gamma ? g[e] : 1.f);
-                if (y)
-                    store_8(y + base + j, v[i]);
-#pragma unroll
-                for (int e = 0; e < 8; e++)
-                    m = max(m, mag(v[i][e]));
-            }
-            if (codes) {
-                m = half_warp_max(m);
-                if (live) {
-                    const float s = block_scale(m);
-                    *reinterpret_cast<uint2 *>(codes + base + j) = codes_8(v[i], Quotient(s));
-                    if (j % kBlock == 0)
-                        scale[row * nb + j / kBlock] = s;
-                }
-            }
+    return ss;
+}
+
+// The outputs of one lane piece whose values are normed already (but for
+// total, which the caller writes); every lane of the warp calls it.
+template <typename T>
+__device__ __forceinline__ void write_piece(const float2 (&v)[kPairs], bool live, int64_t base,
+                                            int j, int64_t row, int nb, T *y, uint8_t *codes,
+                                            float *scale)
+{
+    if (live && y)
+        store_16(y + base + j, v);
+    if (codes) {
+        const float m = eight_lane_max(block_max(v));
+        if (live) {
+            const float s = block_scale(m);
+            *reinterpret_cast<uint4 *>(codes + base + j) = codes_16(v, s);
+            if (j % kBlock == 0)
+                scale[row * nb + j / kBlock] = s;
         }
     }
 }
 
-// Without the norm every block of 128 channels stands by itself: a half warp
-// takes CH of them at a time.
-template <typename T, int CH>
+// Rows of up to 16 tpr values, tpr threads (a multiple of 32) to a row and
+// blockDim / tpr rows at a time; the grid is resident and strides over the
+// rows. A thread's 16 values stay in its registers from the one read to the
+// outputs, so that each byte crosses HBM once and only the sum of squares is
+// exchanged, and its 16 gains for all its rows (read per row they cost more L1
+// traffic than the row). In bf16 the next row is read while this one is
+// written.
+template <typename T>
+__global__ void __launch_bounds__(512, 2)
+add_norm_quant_kernel(const T *x, const T *residual, const float *__restrict__ gamma,
+                      bool gamma_aligned, int64_t rows, int d, int tpr, float eps, T *total, T *y,
+                      uint8_t *codes, float *scale)
+{
+    constexpr bool kAhead = sizeof(T) == 2;
+    __shared__ float part[2][32];
+    const int sub = threadIdx.x % tpr;
+    const int rpb = blockDim.x / tpr;
+    const int j = sub * kLane;
+    const int nb = (d + kBlock - 1) / kBlock;
+    const bool in = j < d;
+    float2 g[kPairs];
+#pragma unroll
+    for (int e = 0; e < kPairs; e++)
+        g[e] = make_float2(1.f, 1.f);
+    if (gamma && in)
+        load_gains(gamma, j, gamma_aligned, g);
+    Raw<T> a, b;
+    int64_t r0 = (int64_t)blockIdx.x * rpb;           // the block's first row
+    const int64_t stride = (int64_t)gridDim.x * rpb, mine = threadIdx.x / tpr;
+    auto read = [&](int64_t row) {
+        if (row < rows && in) {
+            a.load(x + row * d + j);
+            if (residual)
+                b.load(residual + row * d + j);
+        }
+    };
+    if (kAhead)
+        read(r0 + mine);
+    for (int parity = 0; r0 < rows; r0 += stride, parity ^= 1) {
+        const int64_t row = r0 + mine, base = row * d;
+        const bool live = row < rows && in;
+        if (!kAhead)
+            read(row);
+        float2 v[kPairs];
+        float2 ss2 = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int e = 0; e < kPairs; e++) {
+            v[e] = make_float2(0.f, 0.f);
+            if (live)
+                v[e] = residual ? __fadd2_rn(a.pair(e), b.pair(e)) : a.pair(e);
+            ss2 = __ffma2_rn(v[e], v[e], ss2);
+        }
+        if (kAhead)
+            read(row + stride);
+        if (live && total)
+            store_16(total + base + j, v);
+        const float ss = row_sum(ss2.x + ss2.y, tpr, sub, part[parity]);
+        const float inv = 1.f / sqrtf(ss / d + eps);
+#pragma unroll
+        for (int e = 0; e < kPairs; e++)
+            v[e] = __fmul2_rn(__fmul2_rn(v[e], make_float2(inv, inv)), g[e]);
+        write_piece(v, live, base, j, row, nb, y, codes, scale);
+    }
+}
+
+// Longer rows, one to a block, read a second time (from L2) for the outputs.
+constexpr int kLongThreads = 512;
+
+template <typename T>
+__global__ void __launch_bounds__(kLongThreads, 2)
+add_norm_quant_long_kernel(const T *x, const T *residual, const float *__restrict__ gamma,
+                           bool gamma_aligned, int d, float eps, T *total, T *y, uint8_t *codes,
+                           float *scale)
+{
+    __shared__ float part[32];
+    const int64_t row = blockIdx.x, base = row * d;
+    const int nb = (d + kBlock - 1) / kBlock;
+    float2 v[kPairs];
+    auto read = [&](int j) {
+        Raw<T> a, b;
+        if (j < d) {
+            a.load(x + base + j);
+            if (residual)
+                b.load(residual + base + j);
+        }
+#pragma unroll
+        for (int e = 0; e < kPairs; e++) {
+            v[e] = make_float2(0.f, 0.f);
+            if (j < d)
+                v[e] = residual ? __fadd2_rn(a.pair(e), b.pair(e)) : a.pair(e);
+        }
+    };
+    float2 ss2 = make_float2(0.f, 0.f);
+    for (int j0 = 0; j0 < d; j0 += kLongThreads * kLane) {
+        read(j0 + threadIdx.x * kLane);
+#pragma unroll
+        for (int e = 0; e < kPairs; e++)
+            ss2 = __ffma2_rn(v[e], v[e], ss2);
+    }
+    const float ss = row_sum(ss2.x + ss2.y, kLongThreads, threadIdx.x, part);
+    const float inv = 1.f / sqrtf(ss / d + eps);
+    for (int j0 = 0; j0 < d; j0 += kLongThreads * kLane) {
+        const int j = j0 + threadIdx.x * kLane;
+        read(j);
+        if (j < d && total)
+            store_16(total + base + j, v);
+#pragma unroll
+        for (int e = 0; e < kPairs; e++)
+            v[e] = __fmul2_rn(v[e], make_float2(inv, inv));
+        if (gamma && j < d) {
+            float2 g[kPairs];
+            load_gains(gamma, j, gamma_aligned, g);
+#pragma unroll
+            for (int e = 0; e < kPairs; e++)
+                v[e] = __fmul2_rn(v[e], g[e]);
+        }
+        write_piece(v, j < d, base, j, row, nb, y, codes, scale);
+    }
+}
+
+// Without the norm every block of 128 channels stands by itself: 8 lanes take
+// CH of them at a time. FLAT: d is a multiple of 128, so that block g of the
+// whole array is values 128 g ..
+template <typename T, int CH, bool FLAT>
 __global__ void __launch_bounds__(kThreads)
 add_quant_kernel(const T *x, const T *residual, int64_t rows, int d, T *total, T *y,
                  uint8_t *codes, float *scale)
 {
     const int nb = (d + kBlock - 1) / kBlock;
     const int64_t blocks = rows * nb;
-    constexpr int kHalves = kThreads / 16;
-    const int64_t first = (int64_t)blockIdx.x * kHalves * CH + threadIdx.x / 16;
-    Raw8<T> a[CH], b[CH];
-    int64_t at[CH];                                   // this thread's chunk, -1 for none
+    constexpr int kEights = kThreads / 8;
+    const int64_t first = (int64_t)blockIdx.x * kEights * CH + threadIdx.x / 8;
+    const int off = (threadIdx.x & 7) * kLane;
+    const int64_t row0 = FLAT ? 0 : first / nb;
+    const unsigned col0 = FLAT ? 0u : (unsigned)(first - row0 * nb);
+    int64_t at[CH];                                   // this thread's piece, -1 for none
 #pragma unroll
     for (int i = 0; i < CH; i++) {
-        const int64_t g = first + i * kHalves;
-        const int64_t row = g / nb;
-        const int j = (int)(g - row * nb) * kBlock + (threadIdx.x & 15) * 8;
-        at[i] = g < blocks && j < d ? row * d + j : -1;
-        if (at[i] >= 0) {
-            a[i].load(x + at[i]);
-            if (residual)
-                b[i].load(residual + at[i]);
+        const int64_t g = first + i * kEights;
+        if (FLAT) {
+            at[i] = g < blocks ? g * kBlock + off : -1;
+        } else {
+            const unsigned c = col0 + i * kEights, up = c / nb;
+            const int j = (int)(c - up * nb) * kBlock + off;
+            at[i] = g < blocks && j < d ? (row0 + up) * d + j : -1;
         }
+    }
+    float2 v[CH][kPairs];
+    {
+        Raw<T> a[CH], b[CH];
+#pragma unroll
+        for (int i = 0; i < CH; i++) {
+            if (at[i] >= 0) {
+                a[i].load(x + at[i]);
+                if (residual)
+                    b[i].load(residual + at[i]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < CH; i++)
+#pragma unroll
+            for (int e = 0; e < kPairs; e++) {
+                v[i][e] = make_float2(0.f, 0.f);
+                if (at[i] >= 0)
+                    v[i][e] = residual ? __fadd2_rn(a[i].pair(e), b[i].pair(e)) : a[i].pair(e);
+            }
     }
 #pragma unroll
     for (int i = 0; i < CH; i++) {
-        float v[8];
-        uint32_t m = 0;
         if (at[i] >= 0) {
-            a[i].floats(v);
-            if (residual) {
-                float r[8];
-                b[i].floats(r);
-#pragma unroll
-                for (int e = 0; e < 8; e++)
-                    v[e] += r[e];
-                if (total)
-                    store_8(total + at[i], v);
-            }
+            if (total)
+                store_16(total + at[i], v[i]);
             if (y)
-                store_8(y + at[i], v);
-#pragma unroll
-            for (int e = 0; e < 8; e++)
-                m = max(m, mag(v[e]));
+                store_16(y + at[i], v[i]);
         }
         if (codes) {
-            m = half_warp_max(m);
+            const float m = eight_lane_max(block_max(v[i]));
             if (at[i] >= 0) {
                 const float s = block_scale(m);
-                *reinterpret_cast<uint2 *>(codes + at[i]) = codes_8(v, Quotient(s));
-                if ((threadIdx.x & 15) == 0)
-                    scale[first + i * kHalves] = s;
+                *reinterpret_cast<uint4 *>(codes + at[i]) = codes_16(v[i], s);
+                if (off == 0)
+                    scale[first + i * kEights] = s;
             }
         }
     }
 }
 
-// One block of threads per 128 x 128 block of the weight: 16 threads of 8
-// values to a row, 16 rows at a time, held in registers between the maximum
-// and the codes.
+// One block of threads per 128 x 128 block of the weight: 8 lanes to a row, 64
+// rows at a time, two pieces of 16 values a thread, held as they were read
+// between the maximum and the codes (few registers: four such blocks share an
+// SM and hide each other's barrier).
+constexpr int kWeightThreads = 512;
+
 template <typename T>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kWeightThreads)
 quantize_weight_kernel(const T *__restrict__ W, int64_t N, int K, uint8_t *__restrict__ codes,
                        float *__restrict__ scale)
 {
-    __shared__ uint32_t part[kThreads / 32];
+    __shared__ float part[kWeightThreads / 32];
     const int kb = blockIdx.x;
-    const int64_t n0 = (int64_t)blockIdx.y * kBlock;
-    const int col = kb * kBlock + (threadIdx.x & 15) * 8;
-    float v[8][8];
-    uint32_t m = 0;
+    const int64_t n0 = (int64_t)blockIdx.y * kBlock + (threadIdx.x >> 3);
+    const int col = kb * kBlock + (threadIdx.x & 7) * kLane;
+    Raw<T> a[2];
+    bool live[2];
+    float m = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; i++) {
-        const int64_t row = n0 + i * 16 + (threadIdx.x >> 4);
-        if (row < N && col < K) {
-            load_8(W + row * K + col, v[i]);
-#pragma unroll
-            for (int e = 0; e < 8; e++)
-                m = max(m, mag(v[i][e]));
-        }
+    for (int i = 0; i < 2; i++) {
+        live[i] = n0 + i * 64 < N && col < K;
+        if (live[i])
+            a[i].load(W + (n0 + i * 64) * K + col);
     }
 #pragma unroll
+    for (int i = 0; i < 2; i++)
+        if (live[i])
+#pragma unroll
+            for (int e = 0; e < kPairs; e++)
+                m = max_mag(m, a[i].pair(e));
+#pragma unroll
     for (int o = 16; o > 0; o >>= 1)
-        m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
     if ((threadIdx.x & 31) == 0)
         part[threadIdx.x >> 5] = m;
     __syncthreads();
+    m = part[threadIdx.x & 15];
 #pragma unroll
-    for (int i = 0; i < kThreads / 32; i++)
-        m = max(m, part[i]);
+    for (int o = 8; o > 0; o >>= 1)
+        m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
     const float s = block_scale(m);
-    const Quotient q(s);
 #pragma unroll
-    for (int i = 0; i < 8; i++) {
-        const int64_t row = n0 + i * 16 + (threadIdx.x >> 4);
-        if (row < N && col < K)
-            *reinterpret_cast<uint2 *>(codes + row * K + col) = codes_8(v[i], q);
+    for (int i = 0; i < 2; i++) {
+        if (live[i]) {
+            float2 v[kPairs];
+#pragma unroll
+            for (int e = 0; e < kPairs; e++)
+                v[e] = a[i].pair(e);
+            *reinterpret_cast<uint4 *>(codes + (n0 + i * 64) * K + col) = codes_16(v, s);
+        }
     }
     if (threadIdx.x == 0)
         scale[(int64_t)blockIdx.y * gridDim.x + kb] = s;
 }
 
-template <typename T, int CH, bool HOLD>
-void launch_norm(const AddNormQuantArgs &a, int tpr, int rpb, cudaStream_t s)
+template <typename T, bool FLAT>
+cudaError_t launch_quant(const AddNormQuantArgs &a, cudaStream_t s)
 {
-    add_norm_quant_kernel<T, CH, HOLD><<<(unsigned)((a.rows + rpb - 1) / rpb), tpr * rpb, 0, s>>>(
-        (const T *)a.x, (const T *)a.residual, a.gamma, a.rows, a.d, tpr, a.eps, (T *)a.total,
-        (T *)a.y, a.codes, a.scale);
+    constexpr int CH = 2;
+    const int64_t blocks = a.rows * ((a.d + kBlock - 1) / kBlock);
+    const int64_t grid = (blocks + kThreads / 8 * CH - 1) / (kThreads / 8 * CH);
+    if (grid > INT32_MAX)
+        return cudaErrorInvalidConfiguration;
+    add_quant_kernel<T, CH, FLAT><<<(unsigned)grid, kThreads, 0, s>>>(
+        (const T *)a.x, (const T *)a.residual, a.rows, a.d, (T *)a.total, (T *)a.y, a.codes,
+        a.scale);
+    return cudaGetLastError();
 }
 
 template <typename T>
 cudaError_t launch_add_norm_quant_t(const AddNormQuantArgs &a, cudaStream_t s)
 {
-    if (!a.normalise) {
-        constexpr int CH = 4;
-        const int64_t blocks = a.rows * ((a.d + kBlock - 1) / kBlock);
-        const int64_t grid = (blocks + kThreads / 16 * CH - 1) / (kThreads / 16 * CH);
-        if (grid > INT32_MAX)
-            return cudaErrorInvalidConfiguration;
-        add_quant_kernel<T, CH><<<(unsigned)grid, kThreads, 0, s>>>(
-            (const T *)a.x, (const T *)a.residual, a.rows, a.d, (T *)a.total, (T *)a.y, a.codes,
-            a.scale);
+    if (!a.normalise)
+        return a.d % kBlock == 0 ? launch_quant<T, true>(a, s) : launch_quant<T, false>(a, s);
+    const bool ga = ((uintptr_t)a.gamma & 15u) == 0;
+    const int warps = (a.d + 32 * kLane - 1) / (32 * kLane);
+    if (warps * 32 > 512) {
+        add_norm_quant_long_kernel<T><<<(unsigned)a.rows, kLongThreads, 0, s>>>(
+            (const T *)a.x, (const T *)a.residual, a.gamma, ga, a.d, a.eps, (T *)a.total,
+            (T *)a.y, a.codes, a.scale);
         return cudaGetLastError();
     }
-    const int warps = (a.d + 255) / 256;              // of 8 values a lane
-    if (warps <= 8) {
-        const int tpr = 32 * ((warps + 1) / 2);
-        launch_norm<T, 2, true>(a, tpr, 256 / tpr, s);
-    } else if (warps <= 64) {
-        const int tpr = 32 * ((warps + 3) / 4);
-        launch_norm<T, 4, true>(a, tpr, tpr < 256 ? 256 / tpr : 1, s);
-    } else {
-        launch_norm<T, 2, false>(a, 1024, 1, s);
-    }
+    const int tpr = 32 * warps, rpb = warps <= 8 ? 8 / warps : 1;
+    int dev = 0, sms = 148, per_sm = 1;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(
+        &per_sm, add_norm_quant_kernel<T>, tpr * rpb, 0);
+    if (e != cudaSuccess)
+        return e;
+    const int64_t want = (a.rows + rpb - 1) / rpb, room = (int64_t)sms * per_sm;
+    add_norm_quant_kernel<T><<<(unsigned)(want < room ? want : room), tpr * rpb, 0, s>>>(
+        (const T *)a.x, (const T *)a.residual, a.gamma, ga, a.rows, a.d, tpr, a.eps,
+        (T *)a.total, (T *)a.y, a.codes, a.scale);
     return cudaGetLastError();
 }
 
@@ -385,11 +497,11 @@ cudaError_t launch_quantize_weight(const QuantWeightArgs &a, cudaStream_t s)
         const int64_t row0 = b0 * kBlock, rows = a.N - row0;
         const dim3 grid(nbk, (unsigned)nb);
         if (a.dt == CSA_BF16)
-            quantize_weight_kernel<__nv_bfloat16><<<grid, kThreads, 0, s>>>(
+            quantize_weight_kernel<__nv_bfloat16><<<grid, kWeightThreads, 0, s>>>(
                 (const __nv_bfloat16 *)a.W + row0 * a.K, rows, a.K, a.codes + row0 * a.K,
                 a.scale + b0 * nbk);
         else
-            quantize_weight_kernel<float><<<grid, kThreads, 0, s>>>(
+            quantize_weight_kernel<float><<<grid, kWeightThreads, 0, s>>>(
                 (const float *)a.W + row0 * a.K, rows, a.K, a.codes + row0 * a.K,
                 a.scale + b0 * nbk);
     }
