@@ -202,7 +202,7 @@ __device__ __forceinline__ void write_piece(const float2 (&v)[kPairs], bool live
 // traffic than the row). In bf16 the next row is read while this one is
 // written.
 template <typename T>
-__global__ void __launch_bounds__(512, 2)
+__global__ void __launch_bounds__(512, sizeof(T) == 2 ? 2 : 1)
 add_norm_quant_kernel(const T *x, const T *residual, const float *__restrict__ gamma,
                       bool gamma_aligned, int64_t rows, int d, int tpr, float eps, T *total, T *y,
                       uint8_t *codes, float *scale)
@@ -263,7 +263,7 @@ add_norm_quant_kernel(const T *x, const T *residual, const float *__restrict__ g
 constexpr int kLongThreads = 512;
 
 template <typename T>
-__global__ void __launch_bounds__(kLongThreads, 2)
+__global__ void __launch_bounds__(kLongThreads, sizeof(T) == 2 ? 2 : 1)
 add_norm_quant_long_kernel(const T *x, const T *residual, const float *__restrict__ gamma,
                            bool gamma_aligned, int d, float eps, T *total, T *y, uint8_t *codes,
                            float *scale)
@@ -381,55 +381,54 @@ add_quant_kernel(const T *x, const T *residual, int64_t rows, int d, T *total, T
     }
 }
 
-// One block of threads per 128 x 128 block of the weight: 8 lanes to a row, 64
-// rows at a time, two pieces of 16 values a thread, held as they were read
-// between the maximum and the codes (few registers: four such blocks share an
-// SM and hide each other's barrier).
-constexpr int kWeightThreads = 512;
+// One block of threads per 128 x 128 block of the weight: 8 lanes to a row,
+// four pieces of 16 values a thread, held as they were read between the
+// maximum and the codes (in bf16 few enough registers for four such blocks on
+// an SM, which hide each other's barrier).
+constexpr int kPieces = kBlock * kBlock / (kThreads * kLane);
+constexpr int kRowStep = kThreads / 8;
 
 template <typename T>
-__global__ void __launch_bounds__(kWeightThreads)
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2)
 quantize_weight_kernel(const T *__restrict__ W, int64_t N, int K, uint8_t *__restrict__ codes,
                        float *__restrict__ scale)
 {
-    __shared__ float part[kWeightThreads / 32];
+    __shared__ float part[kThreads / 32];
     const int kb = blockIdx.x;
     const int64_t n0 = (int64_t)blockIdx.y * kBlock + (threadIdx.x >> 3);
     const int col = kb * kBlock + (threadIdx.x & 7) * kLane;
-    Raw<T> a[2];
-    bool live[2];
+    Raw<T> a[kPieces];
+#pragma unroll
+    for (int i = 0; i < kPieces; i++) {
+        if (n0 + i * kRowStep < N && col < K)
+            a[i].load(W + (n0 + i * kRowStep) * K + col);
+        else
+            a[i] = Raw<T>{};
+    }
     float m = 0.f;
 #pragma unroll
-    for (int i = 0; i < 2; i++) {
-        live[i] = n0 + i * 64 < N && col < K;
-        if (live[i])
-            a[i].load(W + (n0 + i * 64) * K + col);
-    }
+    for (int i = 0; i < kPieces; i++)
 #pragma unroll
-    for (int i = 0; i < 2; i++)
-        if (live[i])
-#pragma unroll
-            for (int e = 0; e < kPairs; e++)
-                m = max_mag(m, a[i].pair(e));
+        for (int e = 0; e < kPairs; e++)
+            m = max_mag(m, a[i].pair(e));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
         m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
     if ((threadIdx.x & 31) == 0)
         part[threadIdx.x >> 5] = m;
     __syncthreads();
-    m = part[threadIdx.x & 15];
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1)
-        m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+    for (int i = 0; i < kThreads / 32; i++)
+        m = max_nan(m, part[i]);
     const float s = block_scale(m);
 #pragma unroll
-    for (int i = 0; i < 2; i++) {
-        if (live[i]) {
+    for (int i = 0; i < kPieces; i++) {
+        if (n0 + i * kRowStep < N && col < K) {
             float2 v[kPairs];
 #pragma unroll
             for (int e = 0; e < kPairs; e++)
                 v[e] = a[i].pair(e);
-            *reinterpret_cast<uint4 *>(codes + (n0 + i * 64) * K + col) = codes_16(v, s);
+            *reinterpret_cast<uint4 *>(codes + (n0 + i * kRowStep) * K + col) = codes_16(v, s);
         }
     }
     if (threadIdx.x == 0)
@@ -497,11 +496,11 @@ cudaError_t launch_quantize_weight(const QuantWeightArgs &a, cudaStream_t s)
         const int64_t row0 = b0 * kBlock, rows = a.N - row0;
         const dim3 grid(nbk, (unsigned)nb);
         if (a.dt == CSA_BF16)
-            quantize_weight_kernel<__nv_bfloat16><<<grid, kWeightThreads, 0, s>>>(
+            quantize_weight_kernel<__nv_bfloat16><<<grid, kThreads, 0, s>>>(
                 (const __nv_bfloat16 *)a.W + row0 * a.K, rows, a.K, a.codes + row0 * a.K,
                 a.scale + b0 * nbk);
         else
-            quantize_weight_kernel<float><<<grid, kWeightThreads, 0, s>>>(
+            quantize_weight_kernel<float><<<grid, kThreads, 0, s>>>(
                 (const float *)a.W + row0 * a.K, rows, a.K, a.codes + row0 * a.K,
                 a.scale + b0 * nbk);
     }
