@@ -19,10 +19,9 @@
 //
 // Every wait is bounded; on expiry the kernel records CSA_ERR_TIMEOUT, lets
 // its copies and products land and returns.
-#include <float.h>
-
 #include "common.cuh"
 #include "kernels.h"
+#include "quant8.cuh"
 #include "tc.cuh"
 #include "tma_host.h"
 
@@ -43,20 +42,6 @@ struct ProjDev {
     csa_dtype out_dt;
 };
 
-// The e4m3 scale of a block of results whose largest magnitude has the bits m.
-__device__ __forceinline__ float out_block_scale(uint32_t m)
-{
-    const float s = __uint_as_float(m) / 448.0f;
-    return s < FLT_MIN ? FLT_MIN : s;
-}
-
-__device__ __forceinline__ uint32_t mag_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
-
-__device__ __forceinline__ uint32_t codes_4(float a, float b, float c, float d, float s)
-{
-    return float2_to_e4m3x2(a / s, b / s) | (uint32_t)float2_to_e4m3x2(c / s, d / s) << 16;
-}
-
 __device__ __forceinline__ uint32_t bf16_2(float a, float b)
 {
     const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
@@ -68,15 +53,39 @@ __device__ __forceinline__ uint32_t bf16_2(float a, float b)
 // Tiles of 128 tokens x TN features. Warp 0 issues the TMA loads, warp 1 the
 // MMAs, TN / 32 epilogue warps each own a TMEM lane quarter (32 tokens) and
 // 128 features (one output scale's block). Tensor memory holds 512 / TN
-// accumulators of one block each.
+// accumulators of one block each. With TN = 256 the epilogue's threads take
+// registers over from the first warpgroup (40 + 2 x 232 = 3 x 168), so that
+// 128 sums and 64 loaded products fit.
 template <int TN> struct Rows {
     static constexpr int STAGES = TN == 256 ? 4 : 6;
     static constexpr int NBUF = 512 / TN;
     static constexpr int EPI = TN / 32;
-    static constexpr int THREADS = 64 + 32 * EPI;
+    static constexpr int THREADS = 128 + 32 * EPI;
     static constexpr uint32_t A_BYTES = 128 * PB, B_BYTES = TN * PB;
     static constexpr size_t SMEM = 1024 + STAGES * (A_BYTES + B_BYTES) + 256;
 };
+
+// Four consecutive scales' products from block b on (zero behind the last);
+// vec: both rows of scales are 16-byte aligned and nb a multiple of 4.
+__device__ __forceinline__ float4 scale_quad(const float *as, const float *ws, int b, int nb,
+                                             bool live, bool vec)
+{
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (!live || b >= nb)
+        return s;
+    if (vec) {
+        const float4 x = __ldg((const float4 *)(as + b)), w = __ldg((const float4 *)(ws + b));
+        return make_float4(x.x * w.x, x.y * w.y, x.z * w.z, x.w * w.w);
+    }
+    s.x = as[b] * ws[b];
+    if (b + 1 < nb)
+        s.y = as[b + 1] * ws[b + 1];
+    if (b + 2 < nb)
+        s.z = as[b + 2] * ws[b + 2];
+    if (b + 3 < nb)
+        s.w = as[b + 3] * ws[b + 3];
+    return s;
+}
 
 template <int TN>
 __global__ void __launch_bounds__(Rows<TN>::THREADS, 1)
@@ -122,7 +131,6 @@ proj_rows_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     tc::fence_after();
     const uint32_t tmem = *tmem_slot;
     volatile int *abortv = abort_flag;
-
     // tile t -> (group, m tile, n tile), n fastest: the blocks working at one
     // time share their tokens through L2
     auto coords = [&](int64_t t, int &grp, int64_t &mi, int &ni) {
@@ -132,8 +140,10 @@ proj_rows_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         grp = (int)(r / mt);
     };
 
-    if (warp == 0) {
-        if (lane == 0) {
+    if (warp < 4) {
+        if constexpr (TN == 256)
+            tc::regs_down<40>();
+        if (warp == 0 && lane == 0) {
             // ---------------- producer
             uint32_t it = 0;
             bool ok = true;
@@ -163,9 +173,7 @@ proj_rows_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             for (uint32_t j = it > R::STAGES ? it - R::STAGES : 0; j < it; j++)
                 static_cast<void>(tc::mbar_wait(&full[j % R::STAGES], (j / R::STAGES) & 1, &never,
                                                 200000000ull));
-        }
-    } else if (warp == 1) {
-        if (lane == 0) {
+        } else if (warp == 1 && lane == 0) {
             // ---------------- MMA issuer
             constexpr uint32_t idesc = tc::idesc_e4m3(128, TN);
             uint32_t it = 0;
@@ -198,11 +206,15 @@ proj_rows_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             volatile int never = 0;
             static_cast<void>(tc::mbar_wait(done, 0, &never, 200000000ull));
         }
+        __syncwarp();
     } else {
+        if constexpr (TN == 256)
+            tc::regs_up<232>();
         // ---------------- epilogue: lane quarter warp % 4 = 32 tokens, the
         // features part * 128 .. + 127 of the tile
-        const int q4 = warp & 3, part = (warp - 2) >> 2;
+        const int q4 = warp & 3, part = (warp - 4) >> 2;
         const uint32_t lane_addr = tmem + ((uint32_t)(q4 * 32) << 16) + part * 128;
+        const bool vec = a.nb % 4 == 0 && (((uintptr_t)a.As | (uintptr_t)a.Ws) & 15) == 0;
         uint32_t it = 0;
         bool ok = true;
         for (int64_t t = blockIdx.x; t < ntiles && ok; t += gridDim.x) {
@@ -219,10 +231,14 @@ proj_rows_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
 #pragma unroll
             for (int j = 0; j < 64; j++)
                 acc[j] = make_float2(0.f, 0.f);
-            float s = live ? as[0] * ws[0] : 0.f;
+            float4 s4 = scale_quad(as, ws, 0, a.nb, live, vec), next4 = s4;
             for (int b = 0; b < a.nb; b++, it++) {
                 const int buf = it % R::NBUF;
-                const float s_next = live && b + 1 < a.nb ? as[b + 1] * ws[b + 1] : 0.f;
+                if ((b & 3) == 0) {
+                    s4 = next4;
+                    next4 = scale_quad(as, ws, b + 4, a.nb, live, vec);
+                }
+                const float s = b & 2 ? (b & 1 ? s4.w : s4.z) : (b & 1 ? s4.y : s4.x);
                 if (!tc::mbar_wait(&accf[buf], (it / R::NBUF) & 1, abortv)) {
                     *abort_flag = 1;
                     report(a.err, CSA_ERR_TIMEOUT, K_FP8_PROJ, blockIdx.x, 2);
@@ -230,14 +246,14 @@ proj_rows_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                     break;
                 }
                 tc::fence_after();
-                uint32_t v[2][16];
+                uint32_t v[2][32];
                 const float2 s2 = make_float2(s, s);
-                tc::tmem_ld16(lane_addr + buf * TN, v[0]);
+                tc::tmem_ld32(lane_addr + buf * TN, v[0]);
 #pragma unroll
-                for (int c = 0; c < 8; c++) {
+                for (int c = 0; c < 4; c++) {
                     tc::tmem_ld_wait(v[c & 1]);
-                    if (c < 7) {
-                        tc::tmem_ld16(lane_addr + buf * TN + (c + 1) * 16, v[(c + 1) & 1]);
+                    if (c < 3) {
+                        tc::tmem_ld32(lane_addr + buf * TN + (c + 1) * 32, v[(c + 1) & 1]);
                     } else {
                         tc::fence_before();
                         __syncwarp();
@@ -245,13 +261,12 @@ proj_rows_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                             tc::mbar_arrive(&acce[buf]);
                     }
 #pragma unroll
-                    for (int j = 0; j < 8; j++)
-                        acc[c * 8 + j] =
+                    for (int j = 0; j < 16; j++)
+                        acc[c * 16 + j] =
                             __ffma2_rn(make_float2(__uint_as_float(v[c & 1][2 * j]),
                                                    __uint_as_float(v[c & 1][2 * j + 1])),
-                                       s2, acc[c * 8 + j]);
+                                       s2, acc[c * 16 + j]);
                 }
-                s = s_next;
             }
             if (!ok || !live)
                 continue;
@@ -259,7 +274,16 @@ proj_rows_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             const int cols = min(128, a.N - n0);
             if (a.out_dt == CSA_BF16) {
                 __nv_bfloat16 *dst = (__nv_bfloat16 *)a.out + o;
-                if (cols == 128 && a.ldo % 8 == 0) {
+                if (cols == 128 && a.ldo % 16 == 0 && ((uintptr_t)a.out & 31) == 0) {
+#pragma unroll
+                    for (int j = 0; j < 8; j++) {
+                        uint32_t w[8];
+#pragma unroll
+                        for (int e = 0; e < 8; e++)
+                            w[e] = bf16_2(acc[8 * j + e].x, acc[8 * j + e].y);
+                        tc::st_global_32(dst + 16 * j, w);
+                    }
+                } else if (cols == 128 && a.ldo % 8 == 0) {
 #pragma unroll
                     for (int j = 0; j < 16; j++)
                         ((uint4 *)dst)[j] =
@@ -287,23 +311,19 @@ proj_rows_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                             dst[j] = j & 1 ? acc[j / 2].y : acc[j / 2].x;
                 }
             } else {
-                uint32_t m = 0;                        // features behind the last are zero
+                float m = 0.f;                         // features behind the last are zero
 #pragma unroll
                 for (int j = 0; j < 64; j++)
-                    m = max(m, max(mag_bits(acc[j].x), mag_bits(acc[j].y)));
-                const float sc = out_block_scale(m);
+                    m = max_mag(m, acc[j]);
+                const float sc = block_scale(m);
                 a.out_scale[r * a.nbo + fb] = sc;
                 uint4 *dst = (uint4 *)((uint8_t *)a.out + o);
+                uint32_t w[32];
+                codes_of<32>(acc, sc, w);
 #pragma unroll
-                for (int j = 0; j < 8; j++) {          // N is a multiple of 16
-                    uint32_t w[4];
-#pragma unroll
-                    for (int e = 0; e < 4; e++)
-                        w[e] = codes_4(acc[8 * j + 2 * e].x, acc[8 * j + 2 * e].y,
-                                       acc[8 * j + 2 * e + 1].x, acc[8 * j + 2 * e + 1].y, sc);
+                for (int j = 0; j < 8; j++)            // N is a multiple of 16
                     if (16 * j < cols)
-                        dst[j] = make_uint4(w[0], w[1], w[2], w[3]);
-                }
+                        dst[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
             }
         }
     }
@@ -517,15 +537,18 @@ proj_cols_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         const int cols = a.N - n0 - lane * 4;         // features of this lane that exist
         const int64_t t = t0 + j, o = t * a.ldo + (int64_t)grp * a.N + n0 + lane * 4;
         if (a.out_dt == CSA_E4M3) {
-            uint32_t m = max(max(mag_bits(v.x), mag_bits(v.y)), max(mag_bits(v.z), mag_bits(v.w)));
+            const float2 p[2] = {make_float2(v.x, v.y), make_float2(v.z, v.w)};
+            float m = max_mag(max_mag(0.f, p[0]), p[1]);
 #pragma unroll
             for (int f = 16; f > 0; f >>= 1)
-                m = max(m, __shfl_xor_sync(0xffffffffu, m, f));
-            const float s = out_block_scale(m);
+                m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, f));
+            const float s = block_scale(m);
+            uint32_t w[1];
+            codes_of<1>(p, s, w);
             if (lane == 0)
                 a.out_scale[t * a.nbo + fb] = s;
             if (cols > 0)                              // N is a multiple of 16
-                *(uint32_t *)((uint8_t *)a.out + o) = codes_4(v.x, v.y, v.z, v.w, s);
+                *(uint32_t *)((uint8_t *)a.out + o) = w[0];
         } else if (a.ldo % 4 == 0) {
             if (cols > 0) {
                 if (a.out_dt == CSA_BF16)

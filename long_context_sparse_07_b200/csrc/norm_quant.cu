@@ -11,10 +11,9 @@
 // Hence packed pairs of float32 (one instruction for two values), quotients
 // without a division, and 16 consecutive values to a lane, so that a scale's
 // block is 8 lanes and its maximum three shuffles for every 16 values.
-#include <float.h>
-
 #include "common.cuh"
 #include "kernels.h"
+#include "quant8.cuh"
 
 namespace csa {
 
@@ -63,19 +62,6 @@ __device__ __forceinline__ void store_16(float *p, const float2 (&v)[kPairs])
         ((float4 *)p)[i] = make_float4(v[2 * i].x, v[2 * i].y, v[2 * i + 1].x, v[2 * i + 1].y);
 }
 
-// Largest of m and two magnitudes; a NaN wins.
-__device__ __forceinline__ float max_mag(float m, float2 v)
-{
-    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(m), "f"(v.x), "f"(v.y));
-    return m;
-}
-
-__device__ __forceinline__ float max_nan(float a, float b)
-{
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(a) : "f"(a), "f"(b));
-    return a;
-}
-
 // Largest magnitude of a scale's block: 16 values of each of 8 lanes.
 __device__ __forceinline__ float block_max(const float2 (&v)[kPairs], float m = 0.f)
 {
@@ -93,47 +79,10 @@ __device__ __forceinline__ float eight_lane_max(float m)
     return m;
 }
 
-// Scale of a block with the largest magnitude m (a NaN stays one).
-__device__ __forceinline__ float block_scale(float m)
-{
-    const float s = m / 448.0f;
-    return s < FLT_MIN ? FLT_MIN : s;
-}
-
-__device__ __forceinline__ uint16_t codes_2(float2 q)
-{
-    return (uint16_t)__nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3);
-}
-
-// Codes of 16 values of a block with scale s, each from the correctly rounded
-// float32 quotient v / s. Between 2^-100 and 2^100 (where no step below under-
-// or overflows) the quotient is taken as Markstein's theorem gives it: with r
-// the rounded reciprocal and q = v r, q + r (v - q s) rounds to the rounded
-// quotient (P. Markstein, "Computation of elementary functions on the IBM RISC
-// System/6000 processor", 1990): three packed instructions for two values.
-// Other scales (NaN among them) divide.
 __device__ __forceinline__ uint4 codes_16(const float2 (&v)[kPairs], float s)
 {
     uint32_t w[4];
-    if (s >= 0x1p-100f && s <= 0x1p100f) {
-        const float r = 1.f / s;
-        const float2 r2 = make_float2(r, r), s2 = make_float2(-s, -s);
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-            uint32_t h[2];
-#pragma unroll
-            for (int e = 0; e < 2; e++) {
-                const float2 x = v[2 * i + e], q = __fmul2_rn(x, r2);
-                h[e] = codes_2(__ffma2_rn(__ffma2_rn(q, s2, x), r2, q));
-            }
-            w[i] = h[0] | h[1] << 16;
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; i++)
-            w[i] = codes_2(make_float2(v[2 * i].x / s, v[2 * i].y / s)) |
-                   (uint32_t)codes_2(make_float2(v[2 * i + 1].x / s, v[2 * i + 1].y / s)) << 16;
-    }
+    codes_of<4>(v, s, w);
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 

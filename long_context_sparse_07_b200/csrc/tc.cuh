@@ -439,3 +439,28 @@ __device__ __forceinline__ float4 cluster_ld4(const void *local, uint32_t rank)
 
 }  // namespace tc
 }  // namespace csa
+
+namespace csa {
+namespace tc {
+
+// Moves registers between warpgroups: every warp of a warpgroup executes it.
+// The shares after all moves add up to at most the launch's registers.
+template <int N> __device__ __forceinline__ void regs_down()
+{
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N> __device__ __forceinline__ void regs_up()
+{
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// 32 bytes to a 32-byte aligned address: a whole sector.
+__device__ __forceinline__ void st_global_32(void *p, const uint32_t (&w)[8])
+{
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
+                 "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
+}  // namespace tc
+}  // namespace csa
