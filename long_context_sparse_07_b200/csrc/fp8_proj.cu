@@ -40,6 +40,7 @@ struct ProjDev {
     int64_t M, ldo;                // ldo = groups N
     int N, K, groups, nb, las, nbo;  // las = groups nb, nbo = ceil(ldo / 128)
     csa_dtype out_dt;
+    bool tma_out;
 };
 
 __device__ __forceinline__ uint32_t bf16_2(float a, float b)
@@ -50,19 +51,26 @@ __device__ __forceinline__ uint32_t bf16_2(float a, float b)
 
 // ------------------------------------------------------------ many tokens
 
-// Tiles of 128 tokens x TN features. Warp 0 issues the TMA loads, warp 1 the
-// MMAs, TN / 32 epilogue warps each own a TMEM lane quarter (32 tokens) and
-// 128 features (one output scale's block). Tensor memory holds 512 / TN
-// accumulators of one block each. With TN = 256 the epilogue's threads take
-// registers over from the first warpgroup (40 + 2 x 232 = 3 x 168), so that
-// 128 sums and 64 loaded products fit.
-template <int TN> struct Rows {
-    static constexpr int STAGES = TN == 256 ? 4 : 6;
-    static constexpr int NBUF = 512 / TN;
+// Tiles of 128 tokens x TN features. Warp 0 issues the TMA loads, warps 1 and
+// 2 in turn the MMAs, TN / 32 epilogue warps each own a TMEM lane quarter (32
+// tokens) and 128 features (one output scale's block). The MMAs go in units of
+// 128 x UN x 128, each with a tensor-memory buffer of its own. Two issuers,
+// because a thread's waits queue up behind its own uncommitted MMAs: one alone
+// left the tensor pipe idle for 250 of 760 cycles a block. With TN = 256 the
+// epilogue's threads take registers over from the first warpgroup (40 + 2 x
+// 232 = 3 x 168), so that 128 sums and 64 loaded products fit. Results leave
+// through shared memory by TMA stores that run beside the next tile's products
+// (stored from the registers, 32 rows to a store instruction, a tile's results
+// held its epilogue for 6400 cycles, as long as seven blocks of inputs).
+template <int TN, int UN> struct Rows {
+    static constexpr int STAGES = TN == 256 ? 3 : 5;
+    static constexpr int NBUF = 512 / UN;
+    static constexpr int UPB = TN / UN;               // units of a block
     static constexpr int EPI = TN / 32;
     static constexpr int THREADS = 128 + 32 * EPI;
     static constexpr uint32_t A_BYTES = 128 * PB, B_BYTES = TN * PB;
-    static constexpr size_t SMEM = 1024 + STAGES * (A_BYTES + B_BYTES) + 256;
+    static constexpr uint32_t OUT_BYTES = 8192;       // of each epilogue warp: 2 store boxes
+    static constexpr size_t SMEM = 1024 + STAGES * (A_BYTES + B_BYTES) + EPI * OUT_BYTES + 256;
 };
 
 // Four consecutive scales' products from block b on (zero behind the last);
@@ -87,17 +95,18 @@ __device__ __forceinline__ float4 scale_quad(const float *as, const float *ws, i
     return s;
 }
 
-template <int TN>
-__global__ void __launch_bounds__(Rows<TN>::THREADS, 1)
+template <int TN, int UN>
+__global__ void __launch_bounds__(Rows<TN, UN>::THREADS, 1)
 proj_rows_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmW,
-                 const ProjDev a)
+                 const __grid_constant__ CUtensorMap tmO, const ProjDev a)
 {
-    using R = Rows<TN>;
+    using R = Rows<TN, UN>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     uint8_t *sA = sm;
     uint8_t *sB = sm + R::STAGES * R::A_BYTES;
-    uint64_t *full = (uint64_t *)(sB + R::STAGES * R::B_BYTES), *empty = full + R::STAGES;
+    uint8_t *sO = sB + R::STAGES * R::B_BYTES;
+    uint64_t *full = (uint64_t *)(sO + R::EPI * R::OUT_BYTES), *empty = full + R::STAGES;
     uint64_t *accf = empty + R::STAGES, *acce = accf + R::NBUF, *done = acce + R::NBUF;
     uint32_t *tmem_slot = (uint32_t *)(done + 1);
     int *abort_flag = (int *)(tmem_slot + 1);
@@ -110,13 +119,13 @@ proj_rows_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     if (threadIdx.x == 0) {
         for (int i = 0; i < R::STAGES; i++) {
             tc::mbar_init(&full[i], 1);
-            tc::mbar_init(&empty[i], 1);
+            tc::mbar_init(&empty[i], R::UPB);
         }
         for (int i = 0; i < R::NBUF; i++) {
             tc::mbar_init(&accf[i], 1);
-            tc::mbar_init(&acce[i], R::EPI);
+            tc::mbar_init(&acce[i], UN / 32);
         }
-        tc::mbar_init(done, 1);
+        tc::mbar_init(done, 2);
         tc::fence_mbar_init();
         *abort_flag = 0;
         tc::tma_prefetch_desc(&tmA);
@@ -155,7 +164,7 @@ proj_rows_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                 for (int b = 0; b < a.nb; b++, it++) {
                     const int st = it % R::STAGES;
                     if (it >= R::STAGES &&
-                        !tc::mbar_wait(&empty[st], ((it / R::STAGES) - 1) & 1, abortv)) {
+                        !tc::mbar_wait_sleep(&empty[st], ((it / R::STAGES) - 1) & 1, abortv)) {
                         ok = false;
                         break;
                     }
@@ -173,36 +182,47 @@ proj_rows_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             for (uint32_t j = it > R::STAGES ? it - R::STAGES : 0; j < it; j++)
                 static_cast<void>(tc::mbar_wait(&full[j % R::STAGES], (j / R::STAGES) & 1, &never,
                                                 200000000ull));
-        } else if (warp == 1 && lane == 0) {
-            // ---------------- MMA issuer
-            constexpr uint32_t idesc = tc::idesc_e4m3(128, TN);
-            uint32_t it = 0;
+        } else if (warp == 1 || warp == 2) {
+            // ---------------- MMA issuers: the whole warp runs the loop (so that
+            // what it computes stays in uniform registers), one lane issues
+            constexpr uint32_t idesc = tc::idesc_e4m3(128, UN);
+            const uint64_t dA = tc::sdesc_sw128(tc::smem_u32(sA)), dB = tc::sdesc_sw128(tc::smem_u32(sB));
+            uint32_t u = 0;                           // units so far, of both issuers
             bool ok = true;
-            const uint32_t sAa = tc::smem_u32(sA), sBa = tc::smem_u32(sB);
             for (int64_t t = blockIdx.x; t < ntiles && ok; t += gridDim.x) {
-                for (int b = 0; b < a.nb; b++, it++) {
-                    const int st = it % R::STAGES, buf = it % R::NBUF;
-                    if ((it >= R::NBUF &&
-                         !tc::mbar_wait(&acce[buf], ((it / R::NBUF) - 1) & 1, abortv)) ||
-                        !tc::mbar_wait(&full[st], (it / R::STAGES) & 1, abortv)) {
+                for (int i = 0; i < a.nb * R::UPB; i++, u++) {
+                    if ((u & 1) != (uint32_t)(warp - 1))
+                        continue;
+                    const uint32_t it = u / R::UPB, h = u % R::UPB;
+                    const uint32_t st = it % R::STAGES, buf = u % R::NBUF;
+                    if ((u >= R::NBUF &&
+                         !tc::mbar_wait_sleep(&acce[buf], ((u / R::NBUF) - 1) & 1, abortv)) ||
+                        !tc::mbar_wait_sleep(&full[st], (it / R::STAGES) & 1, abortv)) {
                         ok = false;
                         break;
                     }
                     tc::fence_after();
+                    if (tc::elect_one()) {
+                        const uint64_t da = dA + ((st * R::A_BYTES) >> 4);
+                        const uint64_t db = dB + ((st * R::B_BYTES + h * UN * PB) >> 4);
 #pragma unroll
-                    for (int kk = 0; kk < PB / UK; kk++)
-                        tc::mma_f8(tmem + buf * TN,
-                                   tc::sdesc_sw128(sAa + st * R::A_BYTES + kk * UK),
-                                   tc::sdesc_sw128(sBa + st * R::B_BYTES + kk * UK), idesc, kk != 0);
-                    tc::mma_commit(&empty[st]);
-                    tc::mma_commit(&accf[buf]);
+                        for (int kk = 0; kk < PB / UK; kk++)
+                            tc::mma_f8(tmem + buf * UN, da + (kk * UK >> 4), db + (kk * UK >> 4),
+                                       idesc, kk != 0);
+                        tc::mma_commit(&empty[st]);
+                        tc::mma_commit(&accf[buf]);
+                    }
+                    __syncwarp();
                 }
             }
-            if (!ok) {
+            if (!ok && lane == 0) {
                 *abort_flag = 1;
                 report(a.err, CSA_ERR_TIMEOUT, K_FP8_PROJ, blockIdx.x, 1);
             }
-            tc::mma_commit(done);
+            __syncwarp();
+            if (tc::elect_one())
+                tc::mma_commit(done);
+            __syncwarp();
             volatile int never = 0;
             static_cast<void>(tc::mbar_wait(done, 0, &never, 200000000ull));
         }
@@ -213,7 +233,7 @@ proj_rows_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         // ---------------- epilogue: lane quarter warp % 4 = 32 tokens, the
         // features part * 128 .. + 127 of the tile
         const int q4 = warp & 3, part = (warp - 4) >> 2;
-        const uint32_t lane_addr = tmem + ((uint32_t)(q4 * 32) << 16) + part * 128;
+        const uint32_t lane_addr = tmem + ((uint32_t)(q4 * 32) << 16) + part * 128 % UN;
         const bool vec = a.nb % 4 == 0 && (((uintptr_t)a.As | (uintptr_t)a.Ws) & 15) == 0;
         uint32_t it = 0;
         bool ok = true;
@@ -233,13 +253,13 @@ proj_rows_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                 acc[j] = make_float2(0.f, 0.f);
             float4 s4 = scale_quad(as, ws, 0, a.nb, live, vec), next4 = s4;
             for (int b = 0; b < a.nb; b++, it++) {
-                const int buf = it % R::NBUF;
+                const uint32_t u = it * R::UPB + part * 128 / UN, buf = u % R::NBUF;
                 if ((b & 3) == 0) {
                     s4 = next4;
                     next4 = scale_quad(as, ws, b + 4, a.nb, live, vec);
                 }
                 const float s = b & 2 ? (b & 1 ? s4.w : s4.z) : (b & 1 ? s4.y : s4.x);
-                if (!tc::mbar_wait(&accf[buf], (it / R::NBUF) & 1, abortv)) {
+                if (!tc::mbar_wait_sleep(&accf[buf], (u / R::NBUF) & 1, abortv)) {
                     *abort_flag = 1;
                     report(a.err, CSA_ERR_TIMEOUT, K_FP8_PROJ, blockIdx.x, 2);
                     ok = false;
@@ -248,12 +268,12 @@ proj_rows_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                 tc::fence_after();
                 uint32_t v[2][32];
                 const float2 s2 = make_float2(s, s);
-                tc::tmem_ld32(lane_addr + buf * TN, v[0]);
+                tc::tmem_ld32(lane_addr + buf * UN, v[0]);
 #pragma unroll
                 for (int c = 0; c < 4; c++) {
                     tc::tmem_ld_wait(v[c & 1]);
                     if (c < 3) {
-                        tc::tmem_ld32(lane_addr + buf * TN + (c + 1) * 32, v[(c + 1) & 1]);
+                        tc::tmem_ld32(lane_addr + buf * UN + (c + 1) * 32, v[(c + 1) & 1]);
                     } else {
                         tc::fence_before();
                         __syncwarp();
@@ -268,64 +288,91 @@ proj_rows_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                                        s2, acc[c * 16 + j]);
                 }
             }
-            if (!ok || !live)
-                continue;
-            const int64_t o = r * a.ldo + (int64_t)grp * a.N + n0;
+            if (!ok)
+                break;
             const int cols = min(128, a.N - n0);
-            if (a.out_dt == CSA_BF16) {
-                __nv_bfloat16 *dst = (__nv_bfloat16 *)a.out + o;
-                if (cols == 128 && a.ldo % 16 == 0 && ((uintptr_t)a.out & 31) == 0) {
-#pragma unroll
-                    for (int j = 0; j < 8; j++) {
-                        uint32_t w[8];
-#pragma unroll
-                        for (int e = 0; e < 8; e++)
-                            w[e] = bf16_2(acc[8 * j + e].x, acc[8 * j + e].y);
-                        tc::st_global_32(dst + 16 * j, w);
-                    }
-                } else if (cols == 128 && a.ldo % 8 == 0) {
-#pragma unroll
-                    for (int j = 0; j < 16; j++)
-                        ((uint4 *)dst)[j] =
-                            make_uint4(bf16_2(acc[4 * j].x, acc[4 * j].y),
-                                       bf16_2(acc[4 * j + 1].x, acc[4 * j + 1].y),
-                                       bf16_2(acc[4 * j + 2].x, acc[4 * j + 2].y),
-                                       bf16_2(acc[4 * j + 3].x, acc[4 * j + 3].y));
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 128; j++)
-                        if (j < cols)
-                            dst[j] = __float2bfloat16_rn(j & 1 ? acc[j / 2].y : acc[j / 2].x);
-                }
-            } else if (a.out_dt == CSA_F32) {
-                float *dst = (float *)a.out + o;
-                if (cols == 128 && a.ldo % 4 == 0) {
-#pragma unroll
-                    for (int j = 0; j < 32; j++)
-                        ((float4 *)dst)[j] = make_float4(acc[2 * j].x, acc[2 * j].y,
-                                                         acc[2 * j + 1].x, acc[2 * j + 1].y);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 128; j++)
-                        if (j < cols)
-                            dst[j] = j & 1 ? acc[j / 2].y : acc[j / 2].x;
-                }
-            } else {
+            float sc = 1.f;
+            if (a.out_dt == CSA_E4M3) {
                 float m = 0.f;                         // features behind the last are zero
 #pragma unroll
                 for (int j = 0; j < 64; j++)
                     m = max_mag(m, acc[j]);
-                const float sc = block_scale(m);
-                a.out_scale[r * a.nbo + fb] = sc;
-                uint4 *dst = (uint4 *)((uint8_t *)a.out + o);
-                uint32_t w[32];
-                codes_of<32>(acc, sc, w);
+                sc = block_scale(m);
+                if (live)
+                    a.out_scale[r * a.nbo + fb] = sc;
+            }
+            if (a.tma_out) {
+                // boxes of 32 tokens x 128 bytes, two at a time, in the store's
+                // 128-byte swizzle (piece p of row r at p ^ r % 8)
+                uint8_t *stage = sO + (warp - 4) * R::OUT_BYTES;
+                const int x0 = grp * a.N + n0, y0 = (int)(mi * 128 + q4 * 32);
+                const bool rows = y0 < a.M;
+                auto free_stage = [&] {
+                    if (lane == 0)
+                        tc::bulk_wait_read();
+                    __syncwarp();
+                };
+                auto put = [&](int box, int piece, uint4 v) {
+                    *(uint4 *)(stage + box * 4096 + lane * 128 + ((piece ^ (lane & 7)) << 4)) = v;
+                };
+                // `width` values to a box, the first of them at column `first`
+                auto send = [&](int boxes, int width, int first) {
+                    tc::fence_async_shared();
+                    __syncwarp();
+                    if (lane == 0 && rows) {
+                        for (int i = 0; i < boxes; i++)
+                            if (first + i * width < cols)
+                                tc::tma_store_2d(&tmO, stage + i * 4096, x0 + first + i * width, y0);
+                        tc::bulk_commit();
+                    }
+                };
+                free_stage();
+                if (a.out_dt == CSA_BF16) {
 #pragma unroll
-                for (int j = 0; j < 8; j++)            // N is a multiple of 16
-                    if (16 * j < cols)
-                        dst[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+                    for (int j = 0; j < 16; j++)
+                        put(j / 8, j % 8, make_uint4(bf16_2(acc[4 * j].x, acc[4 * j].y),
+                                                     bf16_2(acc[4 * j + 1].x, acc[4 * j + 1].y),
+                                                     bf16_2(acc[4 * j + 2].x, acc[4 * j + 2].y),
+                                                     bf16_2(acc[4 * j + 3].x, acc[4 * j + 3].y)));
+                    send(2, 64, 0);
+                } else if (a.out_dt == CSA_F32) {
+#pragma unroll
+                    for (int h = 0; h < 2; h++) {
+                        if (h)
+                            free_stage();
+#pragma unroll
+                        for (int j = 0; j < 16; j++) {
+                            const float2 p = acc[h * 32 + 2 * j], q = acc[h * 32 + 2 * j + 1];
+                            put(j / 8, j % 8, make_uint4(__float_as_uint(p.x), __float_as_uint(p.y),
+                                                         __float_as_uint(q.x), __float_as_uint(q.y)));
+                        }
+                        send(2, 32, h * 64);
+                    }
+                } else {
+                    uint32_t w[32];
+                    codes_of<32>(acc, sc, w);
+#pragma unroll
+                    for (int j = 0; j < 8; j++)
+                        put(0, j, make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]));
+                    send(1, 128, 0);
+                }
+            } else if (live) {
+                // rows that no tensor map describes (not a multiple of 16 bytes)
+                const int64_t o = r * a.ldo + (int64_t)grp * a.N + n0;
+#pragma unroll
+                for (int j = 0; j < 128; j++) {
+                    const float v = j & 1 ? acc[j / 2].y : acc[j / 2].x;
+                    if (j < cols) {
+                        if (a.out_dt == CSA_BF16)
+                            ((__nv_bfloat16 *)a.out)[o + j] = __float2bfloat16_rn(v);
+                        else
+                            ((float *)a.out)[o + j] = v;
+                    }
+                }
             }
         }
+        if (lane == 0)
+            tc::bulk_wait_all();
     }
     tc::fence_before();
     __syncthreads();
@@ -413,7 +460,7 @@ proj_cols_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             for (; it < nblk; it++) {
                 const int st = it % C::STAGES;
                 if (it >= C::STAGES &&
-                    !tc::mbar_wait(&empty[st], ((it / C::STAGES) - 1) & 1, abortv)) {
+                    !tc::mbar_wait_sleep(&empty[st], ((it / C::STAGES) - 1) & 1, abortv)) {
                     *abort_flag = 1;
                     report(a.err, CSA_ERR_TIMEOUT, K_FP8_PROJ, blockIdx.x, 3);
                     break;
@@ -436,8 +483,8 @@ proj_cols_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             for (uint32_t it = 0; it < nblk; it++) {
                 const int st = it % C::STAGES, buf = it % C::NBUF;
                 if ((it >= C::NBUF &&
-                     !tc::mbar_wait(&acce[buf], ((it / C::NBUF) - 1) & 1, abortv)) ||
-                    !tc::mbar_wait(&full[st], (it / C::STAGES) & 1, abortv)) {
+                     !tc::mbar_wait_sleep(&acce[buf], ((it / C::NBUF) - 1) & 1, abortv)) ||
+                    !tc::mbar_wait_sleep(&full[st], (it / C::STAGES) & 1, abortv)) {
                     *abort_flag = 1;
                     report(a.err, CSA_ERR_TIMEOUT, K_FP8_PROJ, blockIdx.x, 4);
                     break;
@@ -485,7 +532,7 @@ proj_cols_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                 nxt[i] = scale_of(i, it + 1);
             }
             __syncwarp();
-            if (!tc::mbar_wait(&accf[buf], (it / C::NBUF) & 1, abortv)) {
+            if (!tc::mbar_wait_sleep(&accf[buf], (it / C::NBUF) & 1, abortv)) {
                 *abort_flag = 1;
                 report(a.err, CSA_ERR_TIMEOUT, K_FP8_PROJ, blockIdx.x, 5);
                 break;
@@ -591,28 +638,38 @@ int sm_count()
     return sms;
 }
 
-template <int TN>
-cudaError_t launch_rows(const Fp8ProjArgs &g, const ProjDev &d, int sms, cudaStream_t s)
+template <int TN, int UN>
+cudaError_t launch_rows(const Fp8ProjArgs &g, ProjDev d, int sms, cudaStream_t s)
 {
-    using R = Rows<TN>;
-    CUtensorMap tmA, tmW;
+    using R = Rows<TN, UN>;
+    CUtensorMap tmA, tmW, tmO;
     if (!make_tmap_2d(&tmA, g.A, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)g.M,
                       (uint64_t)g.groups * g.K, 128) ||
         !make_tmap_2d(&tmW, g.W, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)d.ldo, (uint64_t)g.K,
                       TN))
         return cudaErrorInvalidValue;
-    cudaError_t e = cudaFuncSetAttribute(proj_rows_kernel<TN>,
+    const int es = g.out_dt == CSA_F32 ? 4 : g.out_dt == CSA_BF16 ? 2 : 1;
+    d.tma_out = d.ldo * es % 16 == 0;
+    tmO = tmA;
+    if (d.tma_out &&
+        !make_tmap_2d(&tmO, g.out,
+                      g.out_dt == CSA_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                      : g.out_dt == CSA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                             : CU_TENSOR_MAP_DATA_TYPE_UINT8,
+                      es, (uint64_t)g.M, (uint64_t)d.ldo, 32))
+        return cudaErrorInvalidValue;
+    cudaError_t e = cudaFuncSetAttribute(proj_rows_kernel<TN, UN>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, (int)R::SMEM);
     if (e != cudaSuccess)
         return e;
     const int64_t tiles = (g.M + 127) / 128 * ((g.N + TN - 1) / TN) * g.groups;
-    proj_rows_kernel<TN><<<(unsigned)(tiles < sms ? tiles : sms), R::THREADS, R::SMEM, s>>>(
-        tmA, tmW, d);
+    proj_rows_kernel<TN, UN><<<(unsigned)(tiles < sms ? tiles : sms), R::THREADS, R::SMEM, s>>>(
+        tmA, tmW, tmO, d);
     return cudaGetLastError();
 }
 
 template <int TT>
-cudaError_t launch_cols(const Fp8ProjArgs &g, const ProjDev &d, int sms, cudaStream_t s)
+cudaError_t launch_cols(const Fp8ProjArgs &g, ProjDev d, int sms, cudaStream_t s)
 {
     using C = Cols<TT>;
     CUtensorMap tmA, tmW;
@@ -661,6 +718,7 @@ cudaError_t launch_fp8_proj(const Fp8ProjArgs &g, unsigned *err, cudaStream_t s)
     d.las = g.groups * d.nb;
     d.nbo = (int)((d.ldo + PB - 1) / PB);
     d.out_dt = g.out_dt;
+    d.tma_out = false;
     const int sms = sm_count();
     // 128 x 128 tiles that the call has
     const int64_t tiles = (g.M + 127) / 128 * ((g.N + 127) / 128) * g.groups;
@@ -673,8 +731,8 @@ cudaError_t launch_fp8_proj(const Fp8ProjArgs &g, unsigned *err, cudaStream_t s)
     if (2 * tiles <= sms)
         return launch_cols<128>(g, d, sms, s);
     if (tiles <= 2 * sms)
-        return launch_rows<128>(g, d, sms, s);
-    return launch_rows<256>(g, d, sms, s);
+        return launch_rows<128, 128>(g, d, sms, s);
+    return launch_rows<256, 128>(g, d, sms, s);
 }
 
 }  // namespace csa

@@ -464,3 +464,70 @@ __device__ __forceinline__ void st_global_32(void *p, const uint32_t (&w)[8])
 
 }  // namespace tc
 }  // namespace csa
+
+namespace csa {
+namespace tc {
+
+// mbar_wait for a pipeline's critical loop: the thread sleeps in the hardware
+// (up to 20 us a try) instead of polling, which slows down every other access
+// to shared memory; the timer is read only after a millisecond of tries.
+__device__ __forceinline__ bool mbar_wait_sleep(uint64_t *bar, uint32_t parity, volatile int *abort)
+{
+#pragma unroll 1
+    for (int i = 0; i < 50; i++) {
+        uint32_t ok;
+        asm volatile("{\n\t.reg .pred P1;\n\t"
+                     "mbarrier.try_wait.parity.shared::cta.b64 P1, [%1], %2, %3;\n\t"
+                     "selp.b32 %0, 1, 0, P1;\n\t}"
+                     : "=r"(ok)
+                     : "r"(smem_u32(bar)), "r"(parity), "r"(20000u)
+                     : "memory");
+        if (ok)
+            return true;
+    }
+    return mbar_wait(bar, parity, abort);
+}
+
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred P1;\n\telect.sync _|P1, 0xffffffff;\n\t"
+                 "selp.b32 %0, 1, 0, P1;\n\t}"
+                 : "=r"(ok));
+    return ok != 0;
+}
+
+}  // namespace tc
+}  // namespace csa
+
+namespace csa {
+namespace tc {
+
+// Box of shared memory to global memory (coordinates not negative; what lies
+// behind the tensor's end is left out), in this thread's current bulk group.
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, const void *src, int x, int y)
+{
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                     (uint64_t)map),
+                 "r"(smem_u32(src)), "r"(x), "r"(y)
+                 : "memory");
+}
+
+__device__ __forceinline__ void bulk_commit()
+{
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+
+// Until this thread's bulk groups have read their shared memory / are complete.
+__device__ __forceinline__ void bulk_wait_read()
+{
+    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+__device__ __forceinline__ void bulk_wait_all()
+{
+    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+
+}  // namespace tc
+}  // namespace csa
