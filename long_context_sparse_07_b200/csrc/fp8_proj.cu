@@ -52,47 +52,46 @@ __device__ __forceinline__ uint32_t bf16_2(float a, float b)
 // ------------------------------------------------------------ many tokens
 
 // Tiles of 128 tokens x TN features. Warp 0 issues the TMA loads, warps 1 and
-// 2 in turn the MMAs, TN / 32 epilogue warps each own a TMEM lane quarter (32
-// tokens) and 128 features (one output scale's block). The MMAs go in units of
-// 128 x UN x 128, each with a tensor-memory buffer of its own. Two issuers,
-// because a thread's waits queue up behind its own uncommitted MMAs: one alone
-// left the tensor pipe idle for 250 of 760 cycles a block. With TN = 256 the
-// epilogue's threads take registers over from the first warpgroup (40 + 2 x
-// 232 = 3 x 168), so that 128 sums and 64 loaded products fit. Results leave
-// through shared memory by TMA stores that run beside the next tile's products
-// (stored from the registers, 32 rows to a store instruction, a tile's results
-// held its epilogue for 6400 cycles, as long as seven blocks of inputs).
+// 2 in turn the MMAs, warp 3 brings the scales, TN / 16 epilogue warps each own
+// a TMEM lane quarter (32 tokens) and 64 features. The MMAs go in units of 128
+// x UN x 128, each with a tensor-memory buffer of its own. Two issuers, because
+// a thread's waits queue up behind its own uncommitted MMAs: one alone left the
+// tensor pipe idle for 250 of 760 cycles a block. Sixteen epilogue warps with
+// 64 sums a thread, because eight with 128 could not overlap their loads from
+// tensor memory (about 300 cycles of its port a block) with their sums (256
+// cycles of the FMA pipe) and took 1050 cycles a block where the MMAs need 512.
+// With TN = 256 the epilogue's threads take registers over from the first
+// warpgroup (32 + 4 x 112 = 5 x 96). Results leave through shared memory by TMA
+// stores that run beside the next tile's products (stored from the registers,
+// 32 rows to a store instruction, a tile's results held its epilogue for 6400
+// cycles, as long as seven blocks of inputs).
 template <int TN, int UN> struct Rows {
     static constexpr int STAGES = TN == 256 ? 3 : 5;
     static constexpr int NBUF = 512 / UN;
     static constexpr int UPB = TN / UN;               // units of a block
-    static constexpr int EPI = TN / 32;
+    static constexpr int EPI = TN / 16;
     static constexpr int THREADS = 128 + 32 * EPI;
     static constexpr uint32_t A_BYTES = 128 * PB, B_BYTES = TN * PB;
-    static constexpr uint32_t OUT_BYTES = 8192;       // of each epilogue warp: 2 store boxes
-    static constexpr size_t SMEM = 1024 + STAGES * (A_BYTES + B_BYTES) + EPI * OUT_BYTES + 256;
+    static constexpr uint32_t OUT_BYTES = 4096;       // of each epilogue warp: a store box
+    // scales of a block: when those of block it are written, its ring stage is
+    // free, so block it - STAGES is multiplied, which took the buffer of the
+    // block NBUF / UPB earlier, which therefore is drained
+    static constexpr int SRING = TN == 256 ? 8 : 16;
+    static_assert(SRING >= STAGES + NBUF / UPB, "scales are overwritten only after their use");
+    static constexpr uint32_t SC_FLOATS = SRING * TN;  // [slot][128-feature half][128 tokens]
+    static constexpr size_t SMEM = 1024 + STAGES * (A_BYTES + B_BYTES) + EPI * OUT_BYTES +
+                                   SC_FLOATS * 4 + EPI * 32 * 4 + 256;
 };
 
-// Four consecutive scales' products from block b on (zero behind the last);
-// vec: both rows of scales are 16-byte aligned and nb a multiple of 4.
-__device__ __forceinline__ float4 scale_quad(const float *as, const float *ws, int b, int nb,
-                                             bool live, bool vec)
+// Scales p[b], p[b + 1] (zero behind the last of nb, or where not live); vec:
+// pairs are 8-byte aligned and nb is even.
+__device__ __forceinline__ float2 scale_pair(const float *p, int b, int nb, bool live, bool vec)
 {
-    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (!live || b >= nb)
-        return s;
-    if (vec) {
-        const float4 x = __ldg((const float4 *)(as + b)), w = __ldg((const float4 *)(ws + b));
-        return make_float4(x.x * w.x, x.y * w.y, x.z * w.z, x.w * w.w);
-    }
-    s.x = as[b] * ws[b];
-    if (b + 1 < nb)
-        s.y = as[b + 1] * ws[b + 1];
-    if (b + 2 < nb)
-        s.z = as[b + 2] * ws[b + 2];
-    if (b + 3 < nb)
-        s.w = as[b + 3] * ws[b + 3];
-    return s;
+    if (!live)
+        return make_float2(0.f, 0.f);
+    if (vec)
+        return __ldg((const float2 *)(p + b));
+    return make_float2(p[b], b + 1 < nb ? p[b + 1] : 0.f);
 }
 
 template <int TN, int UN>
@@ -106,24 +105,25 @@ proj_rows_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     uint8_t *sA = sm;
     uint8_t *sB = sm + R::STAGES * R::A_BYTES;
     uint8_t *sO = sB + R::STAGES * R::B_BYTES;
-    uint64_t *full = (uint64_t *)(sO + R::EPI * R::OUT_BYTES), *empty = full + R::STAGES;
+    float *sS = (float *)(sO + R::EPI * R::OUT_BYTES);
+    float *sM = sS + R::SC_FLOATS;                    // largest magnitudes [epilogue warp][32]
+    uint64_t *full = (uint64_t *)(sM + R::EPI * 32), *empty = full + R::STAGES;
     uint64_t *accf = empty + R::STAGES, *acce = accf + R::NBUF, *done = acce + R::NBUF;
     uint32_t *tmem_slot = (uint32_t *)(done + 1);
     int *abort_flag = (int *)(tmem_slot + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t mt = (a.M + 127) / 128;
-    const int nt = (a.N + TN - 1) / TN;
-    const int64_t ntiles = (int64_t)a.groups * mt * nt;
+    const uint32_t mt = (uint32_t)((a.M + 127) / 128), nt = (uint32_t)((a.N + TN - 1) / TN);
+    const uint32_t ntiles = a.groups * mt * nt;       // below 2^31
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < R::STAGES; i++) {
-            tc::mbar_init(&full[i], 1);
+            tc::mbar_init(&full[i], 2);           // the loads and the scales
             tc::mbar_init(&empty[i], R::UPB);
         }
         for (int i = 0; i < R::NBUF; i++) {
             tc::mbar_init(&accf[i], 1);
-            tc::mbar_init(&acce[i], UN / 32);
+            tc::mbar_init(&acce[i], UN / 16);
         }
         tc::mbar_init(done, 2);
         tc::fence_mbar_init();
@@ -142,25 +142,24 @@ proj_rows_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     volatile int *abortv = abort_flag;
     // tile t -> (group, m tile, n tile), n fastest: the blocks working at one
     // time share their tokens through L2
-    auto coords = [&](int64_t t, int &grp, int64_t &mi, int &ni) {
-        ni = (int)(t % nt);
-        const int64_t r = t / nt;
-        mi = r % mt;
+    auto coords = [&](uint32_t t, int &grp, int &mi, int &ni) {
+        const uint32_t r = t / nt;
+        ni = (int)(t - r * nt);
         grp = (int)(r / mt);
+        mi = (int)(r - grp * mt);
     };
 
     if (warp < 4) {
         if constexpr (TN == 256)
-            tc::regs_down<40>();
+            tc::regs_down<32>();
         if (warp == 0 && lane == 0) {
             // ---------------- producer
             uint32_t it = 0;
             bool ok = true;
-            for (int64_t t = blockIdx.x; t < ntiles && ok; t += gridDim.x) {
-                int grp, ni;
-                int64_t mi;
+            for (uint32_t t = blockIdx.x; t < ntiles && ok; t += gridDim.x) {
+                int grp, mi, ni;
                 coords(t, grp, mi, ni);
-                const int ax = grp * a.K, ay = (int)(mi * 128), wy = grp * a.N + ni * TN;
+                const int ax = grp * a.K, ay = mi * 128, wy = grp * a.N + ni * TN;
                 for (int b = 0; b < a.nb; b++, it++) {
                     const int st = it % R::STAGES;
                     if (it >= R::STAGES &&
@@ -189,15 +188,19 @@ proj_rows_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             const uint64_t dA = tc::sdesc_sw128(tc::smem_u32(sA)), dB = tc::sdesc_sw128(tc::smem_u32(sB));
             uint32_t u = 0;                           // units so far, of both issuers
             bool ok = true;
-            for (int64_t t = blockIdx.x; t < ntiles && ok; t += gridDim.x) {
+            for (uint32_t t = blockIdx.x; t < ntiles && ok; t += gridDim.x) {
                 for (int i = 0; i < a.nb * R::UPB; i++, u++) {
                     if ((u & 1) != (uint32_t)(warp - 1))
                         continue;
                     const uint32_t it = u / R::UPB, h = u % R::UPB;
                     const uint32_t st = it % R::STAGES, buf = u % R::NBUF;
-                    if ((u >= R::NBUF &&
-                         !tc::mbar_wait_sleep(&acce[buf], ((u / R::NBUF) - 1) & 1, abortv)) ||
-                        !tc::mbar_wait_sleep(&full[st], (it / R::STAGES) & 1, abortv)) {
+                    // both barriers tried before either answer is used: one
+                    // round trip to shared memory
+                    const uint32_t pa = ((u / R::NBUF) - 1) & 1, pf = (it / R::STAGES) & 1;
+                    const bool oa = u < R::NBUF || tc::mbar_test_wait(&acce[buf], pa);
+                    const bool of = tc::mbar_test_wait(&full[st], pf);
+                    if ((!oa && !tc::mbar_wait_sleep(&acce[buf], pa, abortv)) ||
+                        (!of && !tc::mbar_wait_sleep(&full[st], pf, abortv))) {
                         ok = false;
                         break;
                     }
@@ -226,55 +229,90 @@ proj_rows_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             volatile int never = 0;
             static_cast<void>(tc::mbar_wait(done, 0, &never, 200000000ull));
         }
+        else if (warp == 3) {
+            // ---------------- scales: the product of a token's and a feature
+            // block's, four of the 128 tokens to a lane, two blocks at a time
+            const bool vec = a.nb % 2 == 0 && (((uintptr_t)a.As | (uintptr_t)a.Ws) & 7) == 0;
+            uint32_t it = 0;
+            bool ok = true;
+            for (uint32_t t = blockIdx.x; t < ntiles && ok; t += gridDim.x) {
+                int grp, mi, ni;
+                coords(t, grp, mi, ni);
+                const int64_t r0 = (int64_t)mi * 128 + lane;
+                const float *as = a.As + r0 * a.las + (int64_t)grp * a.nb;
+                const int n0 = grp * a.N + ni * TN;
+                const float *ws = a.Ws + (int64_t)(n0 / PB) * a.nb;
+                for (int b = 0; b < a.nb && ok; b += 2) {
+                    float2 x[4], w[TN / 128];
+#pragma unroll
+                    for (int i = 0; i < 4; i++)
+                        x[i] = scale_pair(as + (int64_t)i * 32 * a.las, b, a.nb, r0 + i * 32 < a.M,
+                                          vec);
+#pragma unroll
+                    for (int h = 0; h < TN / 128; h++)
+                        w[h] = scale_pair(ws + (int64_t)h * a.nb, b, a.nb,
+                                          ni * TN + h * 128 < a.N, vec);
+#pragma unroll
+                    for (int e = 0; e < 2; e++) {
+                        if (b + e >= a.nb)
+                            break;
+                        const int st = it % R::STAGES;
+                        if (it >= R::STAGES &&
+                            !tc::mbar_wait_sleep(&empty[st], ((it / R::STAGES) - 1) & 1, abortv)) {
+                            ok = false;
+                            break;
+                        }
+                        float *dst = sS + it % R::SRING * TN + lane;
+#pragma unroll
+                        for (int h = 0; h < TN / 128; h++)
+#pragma unroll
+                            for (int i = 0; i < 4; i++)
+                                dst[h * 128 + i * 32] = e ? x[i].y * w[h].y : x[i].x * w[h].x;
+                        __syncwarp();
+                        if (lane == 0)
+                            tc::mbar_arrive(&full[st]);
+                        it++;
+                    }
+                }
+            }
+            if (!ok && lane == 0) {
+                *abort_flag = 1;
+                report(a.err, CSA_ERR_TIMEOUT, K_FP8_PROJ, blockIdx.x, 6);
+            }
+        }
         __syncwarp();
     } else {
         if constexpr (TN == 256)
-            tc::regs_up<232>();
+            tc::regs_up<112>();
         // ---------------- epilogue: lane quarter warp % 4 = 32 tokens, the
-        // features part * 128 .. + 127 of the tile
-        const int q4 = warp & 3, part = (warp - 4) >> 2;
-        const uint32_t lane_addr = tmem + ((uint32_t)(q4 * 32) << 16) + part * 128 % UN;
-        const bool vec = a.nb % 4 == 0 && (((uintptr_t)a.As | (uintptr_t)a.Ws) & 15) == 0;
+        // features c0 .. c0 + 63 of the tile
+        const int e = warp - 4, q4 = warp & 3, c0 = (e >> 2) * 64;
+        const uint32_t lane_addr = tmem + ((uint32_t)(q4 * 32) << 16) + c0 % UN;
+        const float *scales = sS + c0 / 128 * 128 + q4 * 32 + lane;
+        uint8_t *stage = sO + e * R::OUT_BYTES;
+        const int pair = 1 + (e >> 3) * 4 + q4;       // barrier with the warp of the other 64 of 128
         uint32_t it = 0;
-        bool ok = true;
-        for (int64_t t = blockIdx.x; t < ntiles && ok; t += gridDim.x) {
-            int grp, ni;
-            int64_t mi;
-            coords(t, grp, mi, ni);
-            const int64_t r = mi * 128 + q4 * 32 + lane;
-            const int n0 = ni * TN + part * 128;      // first feature, within the group
-            const bool live = r < a.M && n0 < a.N;
-            const int64_t fb = ((int64_t)grp * a.N + n0) / PB;   // its scale block
-            const float *as = a.As + (live ? r * a.las + (int64_t)grp * a.nb : 0);
-            const float *ws = a.Ws + (live ? fb * a.nb : 0);
-            float2 acc[64];
+        for (uint32_t t = blockIdx.x; t < ntiles; t += gridDim.x) {
+            float2 acc[32];
 #pragma unroll
-            for (int j = 0; j < 64; j++)
+            for (int j = 0; j < 32; j++)
                 acc[j] = make_float2(0.f, 0.f);
-            float4 s4 = scale_quad(as, ws, 0, a.nb, live, vec), next4 = s4;
+            bool ok = true;
             for (int b = 0; b < a.nb; b++, it++) {
-                const uint32_t u = it * R::UPB + part * 128 / UN, buf = u % R::NBUF;
-                if ((b & 3) == 0) {
-                    s4 = next4;
-                    next4 = scale_quad(as, ws, b + 4, a.nb, live, vec);
-                }
-                const float s = b & 2 ? (b & 1 ? s4.w : s4.z) : (b & 1 ? s4.y : s4.x);
-                if (!tc::mbar_wait_sleep(&accf[buf], (u / R::NBUF) & 1, abortv)) {
-                    *abort_flag = 1;
-                    report(a.err, CSA_ERR_TIMEOUT, K_FP8_PROJ, blockIdx.x, 2);
-                    ok = false;
+                const uint32_t u = it * R::UPB + c0 / UN, buf = u % R::NBUF;
+                ok = tc::mbar_wait_sleep(&accf[buf], (u / R::NBUF) & 1, abortv);
+                if (!ok)
                     break;
-                }
                 tc::fence_after();
-                uint32_t v[2][32];
+                uint32_t v[32];
+                tc::tmem_ld32(lane_addr + buf * UN, v);
+                // written before the MMAs of this block were let go
+                const float s = scales[it % R::SRING * TN];
                 const float2 s2 = make_float2(s, s);
-                tc::tmem_ld32(lane_addr + buf * UN, v[0]);
 #pragma unroll
-                for (int c = 0; c < 4; c++) {
-                    tc::tmem_ld_wait(v[c & 1]);
-                    if (c < 3) {
-                        tc::tmem_ld32(lane_addr + buf * UN + (c + 1) * 32, v[(c + 1) & 1]);
-                    } else {
+                for (int c = 0; c < 2; c++) {
+                    tc::tmem_ld_wait(v);
+                    if (c == 1) {
                         tc::fence_before();
                         __syncwarp();
                         if (lane == 0)
@@ -282,85 +320,91 @@ proj_rows_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                     }
 #pragma unroll
                     for (int j = 0; j < 16; j++)
-                        acc[c * 16 + j] =
-                            __ffma2_rn(make_float2(__uint_as_float(v[c & 1][2 * j]),
-                                                   __uint_as_float(v[c & 1][2 * j + 1])),
-                                       s2, acc[c * 16 + j]);
+                        acc[c * 16 + j] = __ffma2_rn(
+                            make_float2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])), s2,
+                            acc[c * 16 + j]);
+                    if (c == 0)
+                        tc::tmem_ld32(lane_addr + buf * UN + 32, v);
                 }
+            }
+            if (!ok) {
+                *abort_flag = 1;
+                report(a.err, CSA_ERR_TIMEOUT, K_FP8_PROJ, blockIdx.x, 2);
+            }
+            int grp, mi, ni;
+            coords(t, grp, mi, ni);
+            const int n0 = ni * TN + c0;              // first feature, within the group
+            const int cols = a.N - n0 < 64 ? a.N - n0 : 64;   // may be negative
+            const int col = grp * a.N + n0, y0 = mi * 128 + q4 * 32;
+            if (a.out_dt == CSA_E4M3) {
+                // the scale's block is this warp's 64 features and the other's; both
+                // fill the first one's box
+                uint8_t *box = sO + (e & ~4) * R::OUT_BYTES;
+                float m = 0.f;                         // features behind the last are zero
+#pragma unroll
+                for (int j = 0; j < 32; j++)
+                    m = max_mag(m, acc[j]);
+                sM[e * 32 + lane] = m;
+                if ((e & 4) == 0 && lane == 0)
+                    tc::bulk_wait_read();
+                if (tc::named_bar_or(pair, 64, !ok))
+                    break;
+                const float sc = block_scale(max_nan(m, sM[(e ^ 4) * 32 + lane]));
+                if ((e & 4) == 0 && y0 + lane < a.M && cols > 0)
+                    a.out_scale[(int64_t)(y0 + lane) * a.nbo + col / 128] = sc;
+                uint32_t w[16];
+                codes_of<16>(acc, sc, w);
+#pragma unroll
+                for (int j = 0; j < 4; j++)
+                    *(uint4 *)(box + lane * 128 + ((((e & 4) + j) ^ (lane & 7)) << 4)) =
+                        make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+                tc::fence_async_shared();
+                tc::named_bar_sync(pair, 64);
+                if ((e & 4) == 0 && lane == 0 && y0 < a.M && cols > 0) {
+                    tc::tma_store_2d(&tmO, box, col, y0);
+                    tc::bulk_commit();
+                }
+                continue;
             }
             if (!ok)
                 break;
-            const int cols = min(128, a.N - n0);
-            float sc = 1.f;
-            if (a.out_dt == CSA_E4M3) {
-                float m = 0.f;                         // features behind the last are zero
-#pragma unroll
-                for (int j = 0; j < 64; j++)
-                    m = max_mag(m, acc[j]);
-                sc = block_scale(m);
-                if (live)
-                    a.out_scale[r * a.nbo + fb] = sc;
-            }
             if (a.tma_out) {
-                // boxes of 32 tokens x 128 bytes, two at a time, in the store's
-                // 128-byte swizzle (piece p of row r at p ^ r % 8)
-                uint8_t *stage = sO + (warp - 4) * R::OUT_BYTES;
-                const int x0 = grp * a.N + n0, y0 = (int)(mi * 128 + q4 * 32);
-                const bool rows = y0 < a.M;
-                auto free_stage = [&] {
+                // boxes of 32 tokens x 128 bytes, in the store's 128-byte swizzle
+                // (piece p of row r at p ^ r % 8): one in bf16, two in float32
+#pragma unroll
+                for (int h = 0; h < 2; h++) {
+                    if (h && a.out_dt == CSA_BF16)
+                        break;
                     if (lane == 0)
                         tc::bulk_wait_read();
                     __syncwarp();
-                };
-                auto put = [&](int box, int piece, uint4 v) {
-                    *(uint4 *)(stage + box * 4096 + lane * 128 + ((piece ^ (lane & 7)) << 4)) = v;
-                };
-                // `width` values to a box, the first of them at column `first`
-                auto send = [&](int boxes, int width, int first) {
+#pragma unroll
+                    for (int j = 0; j < 8; j++) {
+                        uint4 w;
+                        if (a.out_dt == CSA_BF16)
+                            w = make_uint4(bf16_2(acc[4 * j].x, acc[4 * j].y),
+                                           bf16_2(acc[4 * j + 1].x, acc[4 * j + 1].y),
+                                           bf16_2(acc[4 * j + 2].x, acc[4 * j + 2].y),
+                                           bf16_2(acc[4 * j + 3].x, acc[4 * j + 3].y));
+                        else
+                            w = make_uint4(__float_as_uint(acc[h * 16 + 2 * j].x),
+                                           __float_as_uint(acc[h * 16 + 2 * j].y),
+                                           __float_as_uint(acc[h * 16 + 2 * j + 1].x),
+                                           __float_as_uint(acc[h * 16 + 2 * j + 1].y));
+                        *(uint4 *)(stage + lane * 128 + ((j ^ (lane & 7)) << 4)) = w;
+                    }
                     tc::fence_async_shared();
                     __syncwarp();
-                    if (lane == 0 && rows) {
-                        for (int i = 0; i < boxes; i++)
-                            if (first + i * width < cols)
-                                tc::tma_store_2d(&tmO, stage + i * 4096, x0 + first + i * width, y0);
+                    if (lane == 0 && y0 < a.M && h * 32 < cols) {
+                        tc::tma_store_2d(&tmO, stage, col + h * 32, y0);
                         tc::bulk_commit();
                     }
-                };
-                free_stage();
-                if (a.out_dt == CSA_BF16) {
-#pragma unroll
-                    for (int j = 0; j < 16; j++)
-                        put(j / 8, j % 8, make_uint4(bf16_2(acc[4 * j].x, acc[4 * j].y),
-                                                     bf16_2(acc[4 * j + 1].x, acc[4 * j + 1].y),
-                                                     bf16_2(acc[4 * j + 2].x, acc[4 * j + 2].y),
-                                                     bf16_2(acc[4 * j + 3].x, acc[4 * j + 3].y)));
-                    send(2, 64, 0);
-                } else if (a.out_dt == CSA_F32) {
-#pragma unroll
-                    for (int h = 0; h < 2; h++) {
-                        if (h)
-                            free_stage();
-#pragma unroll
-                        for (int j = 0; j < 16; j++) {
-                            const float2 p = acc[h * 32 + 2 * j], q = acc[h * 32 + 2 * j + 1];
-                            put(j / 8, j % 8, make_uint4(__float_as_uint(p.x), __float_as_uint(p.y),
-                                                         __float_as_uint(q.x), __float_as_uint(q.y)));
-                        }
-                        send(2, 32, h * 64);
-                    }
-                } else {
-                    uint32_t w[32];
-                    codes_of<32>(acc, sc, w);
-#pragma unroll
-                    for (int j = 0; j < 8; j++)
-                        put(0, j, make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]));
-                    send(1, 128, 0);
                 }
-            } else if (live) {
+            } else if (y0 + lane < a.M) {
                 // rows that no tensor map describes (not a multiple of 16 bytes)
-                const int64_t o = r * a.ldo + (int64_t)grp * a.N + n0;
+                const int64_t o = (int64_t)(y0 + lane) * a.ldo + col;
 #pragma unroll
-                for (int j = 0; j < 128; j++) {
+                for (int j = 0; j < 64; j++) {
                     const float v = j & 1 ? acc[j / 2].y : acc[j / 2].x;
                     if (j < cols) {
                         if (a.out_dt == CSA_BF16)
@@ -663,6 +707,8 @@ cudaError_t launch_rows(const Fp8ProjArgs &g, ProjDev d, int sms, cudaStream_t s
     if (e != cudaSuccess)
         return e;
     const int64_t tiles = (g.M + 127) / 128 * ((g.N + TN - 1) / TN) * g.groups;
+    if (tiles > INT32_MAX)
+        return cudaErrorInvalidConfiguration;
     proj_rows_kernel<TN, UN><<<(unsigned)(tiles < sms ? tiles : sms), R::THREADS, R::SMEM, s>>>(
         tmA, tmW, tmO, d);
     return cudaGetLastError();

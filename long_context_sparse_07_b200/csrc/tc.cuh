@@ -468,23 +468,28 @@ __device__ __forceinline__ void st_global_32(void *p, const uint32_t (&w)[8])
 namespace csa {
 namespace tc {
 
+// One try that sleeps in the hardware for up to `ns` nanoseconds.
+__device__ __forceinline__ bool mbar_try_sleep(uint64_t *bar, uint32_t parity, uint32_t ns = 20000)
+{
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred P1;\n\t"
+                 "mbarrier.try_wait.parity.shared::cta.b64 P1, [%1], %2, %3;\n\t"
+                 "selp.b32 %0, 1, 0, P1;\n\t}"
+                 : "=r"(ok)
+                 : "r"(smem_u32(bar)), "r"(parity), "r"(ns)
+                 : "memory");
+    return ok != 0;
+}
+
 // mbar_wait for a pipeline's critical loop: the thread sleeps in the hardware
 // (up to 20 us a try) instead of polling, which slows down every other access
 // to shared memory; the timer is read only after a millisecond of tries.
 __device__ __forceinline__ bool mbar_wait_sleep(uint64_t *bar, uint32_t parity, volatile int *abort)
 {
 #pragma unroll 1
-    for (int i = 0; i < 50; i++) {
-        uint32_t ok;
-        asm volatile("{\n\t.reg .pred P1;\n\t"
-                     "mbarrier.try_wait.parity.shared::cta.b64 P1, [%1], %2, %3;\n\t"
-                     "selp.b32 %0, 1, 0, P1;\n\t}"
-                     : "=r"(ok)
-                     : "r"(smem_u32(bar)), "r"(parity), "r"(20000u)
-                     : "memory");
-        if (ok)
+    for (int i = 0; i < 50; i++)
+        if (mbar_try_sleep(bar, parity))
             return true;
-    }
     return mbar_wait(bar, parity, abort);
 }
 
