@@ -52,62 +52,57 @@ __device__ __forceinline__ uint32_t bf16_2(float a, float b)
 // ------------------------------------------------------------ many tokens
 
 // Tiles of 128 tokens x TN features. Warp 0 issues the TMA loads, warps 1 and
-// 2 in turn the MMAs, warp 3 brings the scales, TN / 16 epilogue warps each own
-// a TMEM lane quarter (32 tokens) and 64 features. The MMAs go in units of 128
-// x UN x 128, each with a tensor-memory buffer of its own. Two issuers, because
-// a thread's waits queue up behind its own uncommitted MMAs: one alone left the
-// tensor pipe idle for 250 of 760 cycles a block. Sixteen epilogue warps with
-// 64 sums a thread, because eight with 128 could not overlap their loads from
-// tensor memory (about 300 cycles of its port a block) with their sums (256
-// cycles of the FMA pipe) and took 1050 cycles a block where the MMAs need 512.
-// With TN = 256 the epilogue's threads take registers over from the first
-// warpgroup (32 + 4 x 112 = 5 x 96). Results leave through shared memory by TMA
-// stores that run beside the next tile's products (stored from the registers,
-// 32 rows to a store instruction, a tile's results held its epilogue for 6400
-// cycles, as long as seven blocks of inputs).
-template <int TN, int UN> struct Rows {
+// 2 in turn the MMAs of a block, warp 3 copies the scales, TN / 16 epilogue
+// warps each own a TMEM lane quarter (32 tokens) and 64 features. Tensor memory
+// holds 512 / TN accumulators of one block each.
+// Two issuers, because an issuer goes on only when its last MMA has started,
+// and then needs some 450 cycles for its next barriers and issues, which the
+// other's MMAs (512 cycles a block at TN = 256) hide. Sixteen epilogue warps
+// with 64 sums a thread, because eight with 128 could not overlap their loads
+// from tensor memory (about 300 cycles of its port a block) with their sums
+// (256 cycles of the FMA pipe) and took 1050 cycles a block. With TN = 256 the
+// epilogue's threads take registers over from the first warpgroup (32 + 4 x 112
+// = 5 x 96). Scales are copied to shared memory as far ahead as the operands
+// (read by the epilogue itself, or by a warp that loads and then stores them,
+// their latency was the pace: 1000 cycles a block). Results leave through
+// shared memory by TMA stores that run beside the next tile's products (stored
+// from the registers, 32 rows to a store instruction, a tile's results held its
+// epilogue for 6400 cycles, as long as seven blocks of inputs).
+template <int TN> struct Rows {
     static constexpr int STAGES = TN == 256 ? 3 : 5;
-    static constexpr int NBUF = 512 / UN;
-    static constexpr int UPB = TN / UN;               // units of a block
+    static constexpr int NBUF = 512 / TN;
+    // Barriers of landed blocks: twice the stages. An issuer sees every second
+    // block only, and a wait tells a barrier's phases apart by their parity, so
+    // that each barrier has to have the same issuer for good.
+    static constexpr int FULLS = 2 * STAGES;
     static constexpr int EPI = TN / 16;
     static constexpr int THREADS = 128 + 32 * EPI;
     static constexpr uint32_t A_BYTES = 128 * PB, B_BYTES = TN * PB;
     static constexpr uint32_t OUT_BYTES = 4096;       // of each epilogue warp: a store box
-    // scales of a block: when those of block it are written, its ring stage is
+    // scales of a block: when those of block it are copied, its ring stage is
     // free, so block it - STAGES is multiplied, which took the buffer of the
-    // block NBUF / UPB earlier, which therefore is drained
+    // block NBUF earlier, which therefore is drained
     static constexpr int SRING = TN == 256 ? 8 : 16;
-    static_assert(SRING >= STAGES + NBUF / UPB, "scales are overwritten only after their use");
-    static constexpr uint32_t SC_FLOATS = SRING * TN;  // [slot][128-feature half][128 tokens]
+    static_assert(SRING >= STAGES + NBUF, "scales are overwritten only after their use");
+    static constexpr int SLOT = 128 + 4;              // 128 tokens', the features' blocks'
     static constexpr size_t SMEM = 1024 + STAGES * (A_BYTES + B_BYTES) + EPI * OUT_BYTES +
-                                   SC_FLOATS * 4 + EPI * 32 * 4 + 256;
+                                   SRING * SLOT * 4 + EPI * 32 * 4 + 512;
 };
 
-// Scales p[b], p[b + 1] (zero behind the last of nb, or where not live); vec:
-// pairs are 8-byte aligned and nb is even.
-__device__ __forceinline__ float2 scale_pair(const float *p, int b, int nb, bool live, bool vec)
-{
-    if (!live)
-        return make_float2(0.f, 0.f);
-    if (vec)
-        return __ldg((const float2 *)(p + b));
-    return make_float2(p[b], b + 1 < nb ? p[b + 1] : 0.f);
-}
-
-template <int TN, int UN>
-__global__ void __launch_bounds__(Rows<TN, UN>::THREADS, 1)
+template <int TN>
+__global__ void __launch_bounds__(Rows<TN>::THREADS, 1)
 proj_rows_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmW,
                  const __grid_constant__ CUtensorMap tmO, const ProjDev a)
 {
-    using R = Rows<TN, UN>;
+    using R = Rows<TN>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     uint8_t *sA = sm;
     uint8_t *sB = sm + R::STAGES * R::A_BYTES;
     uint8_t *sO = sB + R::STAGES * R::B_BYTES;
     float *sS = (float *)(sO + R::EPI * R::OUT_BYTES);
-    float *sM = sS + R::SC_FLOATS;                    // largest magnitudes [epilogue warp][32]
-    uint64_t *full = (uint64_t *)(sM + R::EPI * 32), *empty = full + R::STAGES;
+    float *sM = sS + R::SRING * R::SLOT;                    // largest magnitudes [epilogue warp][32]
+    uint64_t *full = (uint64_t *)(sM + R::EPI * 32), *empty = full + R::FULLS;
     uint64_t *accf = empty + R::STAGES, *acce = accf + R::NBUF, *done = acce + R::NBUF;
     uint32_t *tmem_slot = (uint32_t *)(done + 1);
     int *abort_flag = (int *)(tmem_slot + 1);
@@ -117,15 +112,15 @@ proj_rows_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     const uint32_t ntiles = a.groups * mt * nt;       // below 2^31
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < R::STAGES; i++) {
-            tc::mbar_init(&full[i], 2);           // the loads and the scales
-            tc::mbar_init(&empty[i], R::UPB);
-        }
+        for (int i = 0; i < R::FULLS; i++)
+            tc::mbar_init(&full[i], 1 + 32);          // the TMA loads, each lane's scales
+        for (int i = 0; i < R::STAGES; i++)
+            tc::mbar_init(&empty[i], 1);
         for (int i = 0; i < R::NBUF; i++) {
             tc::mbar_init(&accf[i], 1);
-            tc::mbar_init(&acce[i], UN / 16);
+            tc::mbar_init(&acce[i], R::EPI);
         }
-        tc::mbar_init(done, 2);
+        tc::mbar_init(done, 2);                       // both issuers
         tc::fence_mbar_init();
         *abort_flag = 0;
         tc::tma_prefetch_desc(&tmA);
@@ -152,8 +147,8 @@ proj_rows_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     if (warp < 4) {
         if constexpr (TN == 256)
             tc::regs_down<32>();
-        if (warp == 0 && lane == 0) {
-            // ---------------- producer
+        if (warp == 0) {
+            // ---------------- operands
             uint32_t it = 0;
             bool ok = true;
             for (uint32_t t = blockIdx.x; t < ntiles && ok; t += gridDim.x) {
@@ -167,56 +162,91 @@ proj_rows_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                         ok = false;
                         break;
                     }
-                    tc::mbar_arrive_expect_tx(&full[st], R::A_BYTES + R::B_BYTES);
-                    tc::tma_load_2d(sA + st * R::A_BYTES, &tmA, &full[st], ax + b * PB, ay);
-                    tc::tma_load_2d(sB + st * R::B_BYTES, &tmW, &full[st], b * PB, wy);
+                    if (tc::elect_one()) {
+                        uint64_t *landed = &full[it % R::FULLS];
+                        tc::mbar_arrive_expect_tx(landed, R::A_BYTES + R::B_BYTES);
+                        tc::tma_load_2d(sA + st * R::A_BYTES, &tmA, landed, ax + b * PB, ay);
+                        tc::tma_load_2d(sB + st * R::B_BYTES, &tmW, landed, b * PB, wy);
+                    }
+                    __syncwarp();
                 }
             }
-            if (!ok) {
+            if (!ok && lane == 0) {
                 *abort_flag = 1;
                 report(a.err, CSA_ERR_TIMEOUT, K_FP8_PROJ, blockIdx.x, 0);
             }
             // let the copies in flight land before the block exits
             volatile int never = 0;
             for (uint32_t j = it > R::STAGES ? it - R::STAGES : 0; j < it; j++)
-                static_cast<void>(tc::mbar_wait(&full[j % R::STAGES], (j / R::STAGES) & 1, &never,
+                static_cast<void>(tc::mbar_wait(&full[j % R::FULLS], (j / R::FULLS) & 1, &never,
                                                 200000000ull));
-        } else if (warp == 1 || warp == 2) {
-            // ---------------- MMA issuers: the whole warp runs the loop (so that
-            // what it computes stays in uniform registers), one lane issues
-            constexpr uint32_t idesc = tc::idesc_e4m3(128, UN);
-            const uint64_t dA = tc::sdesc_sw128(tc::smem_u32(sA)), dB = tc::sdesc_sw128(tc::smem_u32(sB));
-            uint32_t u = 0;                           // units so far, of both issuers
+        } else if (warp == 3) {
+            // ---------------- scales: four tokens' to a lane, and the features'
+            uint32_t it = 0;
             bool ok = true;
             for (uint32_t t = blockIdx.x; t < ntiles && ok; t += gridDim.x) {
-                for (int i = 0; i < a.nb * R::UPB; i++, u++) {
-                    if ((u & 1) != (uint32_t)(warp - 1))
-                        continue;
-                    const uint32_t it = u / R::UPB, h = u % R::UPB;
-                    const uint32_t st = it % R::STAGES, buf = u % R::NBUF;
-                    // both barriers tried before either answer is used: one
-                    // round trip to shared memory
-                    const uint32_t pa = ((u / R::NBUF) - 1) & 1, pf = (it / R::STAGES) & 1;
-                    const bool oa = u < R::NBUF || tc::mbar_test_wait(&acce[buf], pa);
-                    const bool of = tc::mbar_test_wait(&full[st], pf);
-                    if ((!oa && !tc::mbar_wait_sleep(&acce[buf], pa, abortv)) ||
-                        (!of && !tc::mbar_wait_sleep(&full[st], pf, abortv))) {
+                int grp, mi, ni;
+                coords(t, grp, mi, ni);
+                const int64_t r0 = (int64_t)mi * 128 + lane;
+                const int rows = (int)(a.M - r0 < 128 ? a.M - r0 : 128);   // may be negative
+                const float *as = a.As + (rows > 0 ? r0 * a.las + (int64_t)grp * a.nb : 0);
+                const bool has_w = lane < TN / 128 && ni * TN + lane * 128 < a.N;
+                const float *ws =
+                    a.Ws + (has_w ? (int64_t)((grp * a.N + ni * TN) / PB + lane) * a.nb : 0);
+                for (int b = 0; b < a.nb; b++, it++) {
+                    const int st = it % R::STAGES;
+                    if (it >= R::STAGES &&
+                        !tc::mbar_wait_sleep(&empty[st], ((it / R::STAGES) - 1) & 1, abortv)) {
                         ok = false;
                         break;
                     }
-                    tc::fence_after();
-                    if (tc::elect_one()) {
-                        const uint64_t da = dA + ((st * R::A_BYTES) >> 4);
-                        const uint64_t db = dB + ((st * R::B_BYTES + h * UN * PB) >> 4);
+                    // zeros (from any valid address) behind the last row and feature
+                    float *slot = sS + it % R::SRING * R::SLOT;
 #pragma unroll
-                        for (int kk = 0; kk < PB / UK; kk++)
-                            tc::mma_f8(tmem + buf * UN, da + (kk * UK >> 4), db + (kk * UK >> 4),
-                                       idesc, kk != 0);
-                        tc::mma_commit(&empty[st]);
-                        tc::mma_commit(&accf[buf]);
-                    }
-                    __syncwarp();
+                    for (int i = 0; i < 4; i++)
+                        tc::cp_async4(slot + i * 32 + lane,
+                                      i * 32 < rows ? as + (int64_t)i * 32 * a.las + b : a.As,
+                                      i * 32 < rows ? 4 : 0);
+                    if (lane < TN / 128)
+                        tc::cp_async4(slot + 128 + lane, ws + b, has_w ? 4 : 0);
+                    tc::cp_async_arrive(&full[it % R::FULLS]);
                 }
+            }
+            if (!ok && lane == 0) {
+                *abort_flag = 1;
+                report(a.err, CSA_ERR_TIMEOUT, K_FP8_PROJ, blockIdx.x, 6);
+            }
+            tc::cp_async_wait_all();
+        } else {
+            // ---------------- MMA issuers: the whole warp runs the loop (so that
+            // what it computes stays in uniform registers), one lane issues
+            constexpr uint32_t idesc = tc::idesc_e4m3(128, TN);
+            const uint64_t dA = tc::sdesc_sw128(tc::smem_u32(sA)), dB = tc::sdesc_sw128(tc::smem_u32(sB));
+            const uint32_t total = (ntiles - blockIdx.x + gridDim.x - 1) / gridDim.x * a.nb;
+            bool ok = true;
+            for (uint32_t it = warp - 1; it < total; it += 2) {
+                const uint32_t st = it % R::STAGES, buf = it % R::NBUF;
+                const uint32_t pa = (it / R::NBUF - 1) & 1, pf = (it / R::FULLS) & 1;
+                uint64_t *landed = &full[it % R::FULLS];
+                // both barriers tried before either answer is used: one round trip
+                // to shared memory
+                const bool free = it < R::NBUF || tc::mbar_test_wait(&acce[buf], pa);
+                ok = tc::mbar_test_wait(landed, pf) || tc::mbar_wait_sleep(landed, pf, abortv);
+                ok = ok && (free || tc::mbar_wait_sleep(&acce[buf], pa, abortv));
+                if (!ok)
+                    break;
+                tc::fence_after();
+                if (tc::elect_one()) {
+                    const uint64_t da = dA + ((st * R::A_BYTES) >> 4);
+                    const uint64_t db = dB + ((st * R::B_BYTES) >> 4);
+#pragma unroll
+                    for (int kk = 0; kk < PB / UK; kk++)
+                        tc::mma_f8(tmem + buf * TN, da + (kk * UK >> 4), db + (kk * UK >> 4), idesc,
+                                   kk != 0);
+                    tc::mma_commit(&empty[st]);
+                    tc::mma_commit(&accf[buf]);
+                }
+                __syncwarp();
             }
             if (!ok && lane == 0) {
                 *abort_flag = 1;
@@ -229,57 +259,6 @@ proj_rows_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             volatile int never = 0;
             static_cast<void>(tc::mbar_wait(done, 0, &never, 200000000ull));
         }
-        else if (warp == 3) {
-            // ---------------- scales: the product of a token's and a feature
-            // block's, four of the 128 tokens to a lane, two blocks at a time
-            const bool vec = a.nb % 2 == 0 && (((uintptr_t)a.As | (uintptr_t)a.Ws) & 7) == 0;
-            uint32_t it = 0;
-            bool ok = true;
-            for (uint32_t t = blockIdx.x; t < ntiles && ok; t += gridDim.x) {
-                int grp, mi, ni;
-                coords(t, grp, mi, ni);
-                const int64_t r0 = (int64_t)mi * 128 + lane;
-                const float *as = a.As + r0 * a.las + (int64_t)grp * a.nb;
-                const int n0 = grp * a.N + ni * TN;
-                const float *ws = a.Ws + (int64_t)(n0 / PB) * a.nb;
-                for (int b = 0; b < a.nb && ok; b += 2) {
-                    float2 x[4], w[TN / 128];
-#pragma unroll
-                    for (int i = 0; i < 4; i++)
-                        x[i] = scale_pair(as + (int64_t)i * 32 * a.las, b, a.nb, r0 + i * 32 < a.M,
-                                          vec);
-#pragma unroll
-                    for (int h = 0; h < TN / 128; h++)
-                        w[h] = scale_pair(ws + (int64_t)h * a.nb, b, a.nb,
-                                          ni * TN + h * 128 < a.N, vec);
-#pragma unroll
-                    for (int e = 0; e < 2; e++) {
-                        if (b + e >= a.nb)
-                            break;
-                        const int st = it % R::STAGES;
-                        if (it >= R::STAGES &&
-                            !tc::mbar_wait_sleep(&empty[st], ((it / R::STAGES) - 1) & 1, abortv)) {
-                            ok = false;
-                            break;
-                        }
-                        float *dst = sS + it % R::SRING * TN + lane;
-#pragma unroll
-                        for (int h = 0; h < TN / 128; h++)
-#pragma unroll
-                            for (int i = 0; i < 4; i++)
-                                dst[h * 128 + i * 32] = e ? x[i].y * w[h].y : x[i].x * w[h].x;
-                        __syncwarp();
-                        if (lane == 0)
-                            tc::mbar_arrive(&full[st]);
-                        it++;
-                    }
-                }
-            }
-            if (!ok && lane == 0) {
-                *abort_flag = 1;
-                report(a.err, CSA_ERR_TIMEOUT, K_FP8_PROJ, blockIdx.x, 6);
-            }
-        }
         __syncwarp();
     } else {
         if constexpr (TN == 256)
@@ -287,8 +266,7 @@ proj_rows_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         // ---------------- epilogue: lane quarter warp % 4 = 32 tokens, the
         // features c0 .. c0 + 63 of the tile
         const int e = warp - 4, q4 = warp & 3, c0 = (e >> 2) * 64;
-        const uint32_t lane_addr = tmem + ((uint32_t)(q4 * 32) << 16) + c0 % UN;
-        const float *scales = sS + c0 / 128 * 128 + q4 * 32 + lane;
+        const uint32_t lane_addr = tmem + ((uint32_t)(q4 * 32) << 16) + c0;
         uint8_t *stage = sO + e * R::OUT_BYTES;
         const int pair = 1 + (e >> 3) * 4 + q4;       // barrier with the warp of the other 64 of 128
         uint32_t it = 0;
@@ -299,19 +277,19 @@ proj_rows_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                 acc[j] = make_float2(0.f, 0.f);
             bool ok = true;
             for (int b = 0; b < a.nb; b++, it++) {
-                const uint32_t u = it * R::UPB + c0 / UN, buf = u % R::NBUF;
-                ok = tc::mbar_wait_sleep(&accf[buf], (u / R::NBUF) & 1, abortv);
+                const uint32_t buf = it % R::NBUF;
+                ok = tc::mbar_wait_sleep(&accf[buf], (it / R::NBUF) & 1, abortv);
                 if (!ok)
                     break;
                 tc::fence_after();
-                uint32_t v[32];
-                tc::tmem_ld32(lane_addr + buf * UN, v);
-                // written before the MMAs of this block were let go
-                const float s = scales[it % R::SRING * TN];
+                // landed before the MMAs of this block were let go
+                const float *slot = sS + it % R::SRING * R::SLOT;
+                const float s = slot[q4 * 32 + lane] * slot[128 + c0 / 128];
                 const float2 s2 = make_float2(s, s);
 #pragma unroll
                 for (int c = 0; c < 2; c++) {
-                    tc::tmem_ld_wait(v);
+                    uint32_t v[32];
+                    tc::tmem_get(lane_addr + buf * TN + c * 32, v);
                     if (c == 1) {
                         tc::fence_before();
                         __syncwarp();
@@ -323,8 +301,6 @@ proj_rows_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                         acc[c * 16 + j] = __ffma2_rn(
                             make_float2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])), s2,
                             acc[c * 16 + j]);
-                    if (c == 0)
-                        tc::tmem_ld32(lane_addr + buf * UN + 32, v);
                 }
             }
             if (!ok) {
@@ -682,10 +658,10 @@ int sm_count()
     return sms;
 }
 
-template <int TN, int UN>
+template <int TN>
 cudaError_t launch_rows(const Fp8ProjArgs &g, ProjDev d, int sms, cudaStream_t s)
 {
-    using R = Rows<TN, UN>;
+    using R = Rows<TN>;
     CUtensorMap tmA, tmW, tmO;
     if (!make_tmap_2d(&tmA, g.A, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)g.M,
                       (uint64_t)g.groups * g.K, 128) ||
@@ -702,14 +678,14 @@ cudaError_t launch_rows(const Fp8ProjArgs &g, ProjDev d, int sms, cudaStream_t s
                                              : CU_TENSOR_MAP_DATA_TYPE_UINT8,
                       es, (uint64_t)g.M, (uint64_t)d.ldo, 32))
         return cudaErrorInvalidValue;
-    cudaError_t e = cudaFuncSetAttribute(proj_rows_kernel<TN, UN>,
+    cudaError_t e = cudaFuncSetAttribute(proj_rows_kernel<TN>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, (int)R::SMEM);
     if (e != cudaSuccess)
         return e;
     const int64_t tiles = (g.M + 127) / 128 * ((g.N + TN - 1) / TN) * g.groups;
     if (tiles > INT32_MAX)
         return cudaErrorInvalidConfiguration;
-    proj_rows_kernel<TN, UN><<<(unsigned)(tiles < sms ? tiles : sms), R::THREADS, R::SMEM, s>>>(
+    proj_rows_kernel<TN><<<(unsigned)(tiles < sms ? tiles : sms), R::THREADS, R::SMEM, s>>>(
         tmA, tmW, tmO, d);
     return cudaGetLastError();
 }
@@ -777,8 +753,8 @@ cudaError_t launch_fp8_proj(const Fp8ProjArgs &g, unsigned *err, cudaStream_t s)
     if (2 * tiles <= sms)
         return launch_cols<128>(g, d, sms, s);
     if (tiles <= 2 * sms)
-        return launch_rows<128, 128>(g, d, sms, s);
-    return launch_rows<256, 128>(g, d, sms, s);
+        return launch_rows<128>(g, d, sms, s);
+    return launch_rows<256>(g, d, sms, s);
 }
 
 }  // namespace csa
