@@ -282,47 +282,48 @@ def csa_grouped_out_proj(o, Wg, Wo, g: int, u, out, stream=None):
                                        _ptr(out), _stream(stream)))
 
 
-def _operands(what: str, *named):
-    """Checks (name, tensor or None, dtypes, shape) operands of one call: dense
-    CUDA tensors of one device, of a listed dtype and shape. Returns the device
-    index and the pointers (None for None)."""
-    devs, ptrs = set(), []
-    for name, t, dtypes, shape in named:
+_PLAIN = (torch.bfloat16, torch.float32)
+_CODES = (torch.float8_e4m3fn, torch.uint8)
+_DTYPE_CODE = {torch.float32: CSA_F32, torch.bfloat16: CSA_BF16, torch.float8_e4m3fn: CSA_E4M3,
+               torch.uint8: CSA_E4M3}
+
+
+def _operand(t, dtypes, shape, dev):
+    """Device pointer of an operand that is as a call needs it, else 0: a dense
+    tensor of a listed dtype and of this shape, on CUDA device `dev`."""
+    if (t.dtype in dtypes and t.shape == shape and t.is_contiguous() and t.get_device() == dev
+            and dev >= 0):
+        return t.data_ptr() or _EMPTY
+    return 0
+
+
+_EMPTY = 16          # stands for the null address of a tensor without elements
+
+
+def _refuse(what: str, dev: int, **operands):
+    """Raises what is wrong with the first of name = (tensor, dtypes, shape)."""
+    for name, (t, dtypes, shape) in operands.items():
         if t is None:
-            ptrs.append(None)
             continue
         if t.dtype not in dtypes:
             raise TypeError("%s: %s is %s" % (what, name, t.dtype))
-        if t.shape != shape:
-            raise ValueError("%s: %s is %s, expected %s" % (what, name, tuple(t.shape), shape))
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError("%s: %s is %s, expected %s" % (what, name, tuple(t.shape),
+                                                            tuple(shape)))
         if not t.is_contiguous():
             raise ValueError("%s: %s must be contiguous" % (what, name))
-        devs.add(t.get_device())
-        ptrs.append(t.data_ptr())
-    dev = devs.pop()
-    if devs or dev < 0:
-        raise ValueError("%s: operands must be on one CUDA device" % what)
-    return dev, ptrs
+    raise ValueError("%s: operands must be on one CUDA device" % what)
 
 
-def _call_on(dev: int, fn, *args, stream=None):
-    """Calls fn(*args, stream) with `dev` current (its current stream when none
-    is given)."""
-    if dev == torch.cuda.current_device():
-        _check(fn(*args, _stream(stream)))
-    else:
+def _call_on(dev: int, fn, stream, *args):
+    """Calls fn(*args, stream) with `dev` current, on its current stream when
+    none is given."""
+    if dev != torch.cuda.current_device():
         with torch.cuda.device(dev):
-            _check(fn(*args, _stream(stream)))
-
-
-_PLAIN = (torch.bfloat16, torch.float32)
-_F32 = (torch.float32,)
-_CODES = (torch.float8_e4m3fn, torch.uint8)
-
-
-def _blocks(n: int) -> int:
-    """Blocks of 128 that n values make."""
-    return (n + 127) // 128
+            return _call_on(dev, fn, stream, *args)
+    s = torch._C._cuda_getCurrentRawStream(dev) if stream is None else \
+        getattr(stream, "cuda_stream", stream)
+    _check(fn(*args, s))
 
 
 def csa_add_norm_quant(x, residual=None, gamma=None, normalise: bool = True, eps: float = 1e-6,
@@ -330,43 +331,63 @@ def csa_add_norm_quant(x, residual=None, gamma=None, normalise: bool = True, eps
     """total <- x + residual, its RMSNorm (times gamma) to y and, in e4m3 with
     a scale per 128 channels, to codes and scale; x [..., d]. Outputs that are
     None are not written."""
-    shape = tuple(x.shape)
+    shape = x.shape
     d = shape[-1]
-    same = (x.dtype,)
-    dev, (px, pr, pg, pt, py, pc, ps) = _operands(
-        "csa_add_norm_quant", ("x", x, _PLAIN, shape), ("residual", residual, same, shape),
-        ("gamma", gamma, _F32, (d,)), ("total", total, same, shape), ("y", y, same, shape),
-        ("codes", codes, _CODES, shape), ("scale", scale, _F32, shape[:-1] + (_blocks(d),)))
-    _call_on(dev, load().csa_add_norm_quant, px, pr, pg, dtype_code(x), x.numel() // d if d else 0,
-             d, int(bool(normalise)), eps, pt, py, pc, ps, stream=stream)
+    same, dev = (x.dtype,), x.get_device()
+    blocks = shape[:-1] + ((d + 127) >> 7,)
+    px = _operand(x, _PLAIN, shape, dev)
+    pr = None if residual is None else _operand(residual, same, shape, dev)
+    pg = None if gamma is None else _operand(gamma, _PLAIN[1:], (d,), dev)
+    pt = None if total is None else _operand(total, same, shape, dev)
+    py = None if y is None else _operand(y, same, shape, dev)
+    pc = None if codes is None else _operand(codes, _CODES, shape, dev)
+    ps = None if scale is None else _operand(scale, _PLAIN[1:], blocks, dev)
+    if 0 in (px, pr, pg, pt, py, pc, ps):
+        _refuse("csa_add_norm_quant", dev, x=(x, _PLAIN, shape), residual=(residual, same, shape),
+                gamma=(gamma, _PLAIN[1:], (d,)), total=(total, same, shape), y=(y, same, shape),
+                codes=(codes, _CODES, shape), scale=(scale, _PLAIN[1:], blocks))
+    _call_on(dev, load().csa_add_norm_quant, stream, px, pr, pg, _DTYPE_CODE[x.dtype],
+             x.numel() // d if d else 0, d, 1 if normalise else 0, eps, pt, py, pc, ps)
 
 
 def csa_quantize_weight(W, codes, scale, stream=None):
     """W [N, K] to e4m3 codes [N, K] with a scale per 128 x 128 block,
     [ceil(N / 128), ceil(K / 128)]."""
     N, K = W.shape
-    dev, (pw, pc, ps) = _operands(
-        "csa_quantize_weight", ("W", W, _PLAIN, (N, K)), ("codes", codes, _CODES, (N, K)),
-        ("scale", scale, _F32, (_blocks(N), _blocks(K))))
-    _call_on(dev, load().csa_quantize_weight, pw, dtype_code(W), N, K, pc, ps, stream=stream)
+    dev = W.get_device()
+    blocks = ((N + 127) >> 7, (K + 127) >> 7)
+    pw = _operand(W, _PLAIN, (N, K), dev)
+    pc = _operand(codes, _CODES, (N, K), dev)
+    ps = _operand(scale, _PLAIN[1:], blocks, dev)
+    if not (pw and pc and ps):
+        _refuse("csa_quantize_weight", dev, W=(W, _PLAIN, (N, K)), codes=(codes, _CODES, (N, K)),
+                scale=(scale, _PLAIN[1:], blocks))
+    _call_on(dev, load().csa_quantize_weight, stream, pw, _DTYPE_CODE[W.dtype], N, K, pc, ps)
 
 
 def csa_fp8_proj(A, A_scale, W, W_scale, out, out_scale=None, groups: int = 1, stream=None):
     """out [M, groups N] = A [M, groups K] times W [groups N, K] (group by
     group), e4m3 operands with block scales; out bf16, f32, or e4m3 codes with
     out_scale [M, ceil(groups N / 128)]."""
-    M, K = A.shape[0], W.shape[1]
-    GN = W.shape[0]
+    M = A.shape[0]
+    GN, K = W.shape
     if groups < 1 or GN % groups:
         raise ValueError("csa_fp8_proj: groups must divide the rows of W")
-    nb = _blocks(K)
-    dev, (pa, pas, pw, pws, po, pos) = _operands(
-        "csa_fp8_proj", ("A", A, _CODES, (M, groups * K)),
-        ("A_scale", A_scale, _F32, (M, groups * nb)), ("W", W, _CODES, (GN, K)),
-        ("W_scale", W_scale, _F32, (_blocks(GN), nb)), ("out", out, _PLAIN + _CODES, (M, GN)),
-        ("out_scale", out_scale, _F32, (M, _blocks(GN))))
-    _call_on(dev, load().csa_fp8_proj, pa, pas, pw, pws, M, GN // groups, K, groups,
-             dtype_code(out), po, pos, stream=stream)
+    dev = A.get_device()
+    nb, nbo = (K + 127) >> 7, (GN + 127) >> 7
+    pa = _operand(A, _CODES, (M, groups * K), dev)
+    pas = _operand(A_scale, _PLAIN[1:], (M, groups * nb), dev)
+    pw = _operand(W, _CODES, (GN, K), dev)
+    pws = _operand(W_scale, _PLAIN[1:], (nbo, nb), dev)
+    po = _operand(out, _DTYPE_CODE, (M, GN), dev)
+    pos = None if out_scale is None else _operand(out_scale, _PLAIN[1:], (M, nbo), dev)
+    if not (pa and pas and pw and pws and po) or pos == 0:
+        _refuse("csa_fp8_proj", dev, A=(A, _CODES, (M, groups * K)),
+                A_scale=(A_scale, _PLAIN[1:], (M, groups * nb)), W=(W, _CODES, (GN, K)),
+                W_scale=(W_scale, _PLAIN[1:], (nbo, nb)), out=(out, _DTYPE_CODE, (M, GN)),
+                out_scale=(out_scale, _PLAIN[1:], (M, nbo)))
+    _call_on(dev, load().csa_fp8_proj, stream, pa, pas, pw, pws, M, GN // groups, K, groups,
+             _DTYPE_CODE[out.dtype], po, pos)
 
 
 def csa_debug_wait_probe(limit_ns: int, stream=None):

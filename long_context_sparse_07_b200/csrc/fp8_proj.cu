@@ -408,20 +408,25 @@ proj_rows_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
 // cluster's thread blocks. Warps as above, with four epilogue warps (a lane
 // quarter = 32 features each); an epilogue thread owns one feature and all TT
 // tokens. In the end a warp takes one token at a time and adds the cluster's
-// partial results of its 128 features.
+// partial results of its 128 features. Two blocks of threads fit an SM.
+constexpr int kMaxSplit = 8;       // thread blocks of a cluster
+
 template <int TT> struct Cols {
-    static constexpr int STAGES = TT == 16 ? 5 : TT == 32 ? 5 : TT == 64 ? 4 : 6;
-    static constexpr int NBUF = TT == 128 ? 2 : 4;
-    static constexpr int THREADS = 192;
+    static constexpr int STAGES = TT == 64 ? 4 : 5;
+    static constexpr int FULLS = 2 * STAGES;          // as above
+    static constexpr int NBUF = 4;
+    static constexpr int THREADS = 256;
     static constexpr uint32_t W_BYTES = 128 * PB, T_BYTES = TT * PB;
     static constexpr uint32_t TMEM = NBUF * TT;
+    static constexpr int SRING = STAGES + NBUF;       // as above
+    static constexpr int SLOT = TT + 4;               // the tokens' scales, the features'
     static constexpr size_t RING = STAGES * (W_BYTES + T_BYTES);
-    static constexpr size_t SMEM = 1024 + RING + 4 * 2 * TT * 4 + 256;
+    static constexpr size_t SMEM = 1024 + RING + SRING * SLOT * 4 + 256;
     static_assert(RING >= (size_t)TT * 128 * 4, "partial results reuse the ring");
 };
 
 template <int TT>
-__global__ void __launch_bounds__(Cols<TT>::THREADS)
+__global__ void __launch_bounds__(Cols<TT>::THREADS, 2)
 proj_cols_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmW,
                  const ProjDev a, const int split)
 {
@@ -430,8 +435,8 @@ proj_cols_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     uint8_t *sm = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     uint8_t *sW = sm;
     uint8_t *sT = sm + C::STAGES * C::W_BYTES;
-    float *sc = (float *)(sm + C::RING);              // [epilogue warp][2][TT]
-    uint64_t *full = (uint64_t *)(sc + 4 * 2 * TT), *empty = full + C::STAGES;
+    float *sS = (float *)(sm + C::RING);
+    uint64_t *full = (uint64_t *)(sS + C::SRING * C::SLOT), *empty = full + C::FULLS;
     uint64_t *accf = empty + C::STAGES, *acce = accf + C::NBUF, *done = acce + C::NBUF;
     uint32_t *tmem_slot = (uint32_t *)(done + 1);
     int *abort_flag = (int *)(tmem_slot + 1);
@@ -439,11 +444,10 @@ proj_cols_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = split > 1 ? (int)tc::cluster_rank() : 0;
-    const int64_t tile = blockIdx.x / split;
-    const int ft = (a.N + 127) / 128;
-    const int64_t tt = (a.M + TT - 1) / TT;
+    const uint32_t tile = blockIdx.x / split;
+    const uint32_t ft = (a.N + 127) / 128, tt = (uint32_t)((a.M + TT - 1) / TT);
     const int n0 = (int)(tile % ft) * 128;            // first feature, within the group
-    const int64_t t0 = tile / ft % tt * TT;           // first token
+    const int t0 = (int)(tile / ft % tt) * TT;        // first token
     const int grp = (int)(tile / ft / tt);
     const int b0 = (int)((int64_t)a.nb * rank / split);
     const int b1 = (int)((int64_t)a.nb * (rank + 1) / split);
@@ -451,15 +455,15 @@ proj_cols_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     const int64_t fb = ((int64_t)grp * a.N + n0) / PB;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < C::STAGES; i++) {
-            tc::mbar_init(&full[i], 1);
+        for (int i = 0; i < C::FULLS; i++)
+            tc::mbar_init(&full[i], 1 + 32);          // the TMA loads, each lane's scales
+        for (int i = 0; i < C::STAGES; i++)
             tc::mbar_init(&empty[i], 1);
-        }
         for (int i = 0; i < C::NBUF; i++) {
             tc::mbar_init(&accf[i], 1);
             tc::mbar_init(&acce[i], 4);
         }
-        tc::mbar_init(done, 1);
+        tc::mbar_init(done, 2);                       // both issuers
         tc::fence_mbar_init();
         *abort_flag = 0;
     }
@@ -473,106 +477,123 @@ proj_cols_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     const uint32_t tmem = *tmem_slot;
     volatile int *abortv = abort_flag;
 
-    if (warp == 0) {
-        if (lane == 0) {
-            // ---------------- producer
-            uint32_t it = 0;
-            for (; it < nblk; it++) {
-                const int st = it % C::STAGES;
-                if (it >= C::STAGES &&
-                    !tc::mbar_wait_sleep(&empty[st], ((it / C::STAGES) - 1) & 1, abortv)) {
+    if (warp == 0 || warp == 3) {
+        // ---------------- operands (warp 0) and scales (warp 3)
+        const int rows = (int)(a.M - t0 < TT ? a.M - t0 : TT);
+        const float *as = a.As + (lane < rows ? (int64_t)(t0 + lane) * a.las : 0) +
+                          (int64_t)grp * a.nb + b0;
+        const float *ws = a.Ws + fb * a.nb + b0;
+        uint32_t it = 0;
+        for (; it < nblk; it++) {
+            const uint32_t st = it % C::STAGES;
+            if (it >= C::STAGES &&
+                !tc::mbar_wait_sleep(&empty[st], ((it / C::STAGES) - 1) & 1, abortv)) {
+                if (lane == 0) {
                     *abort_flag = 1;
                     report(a.err, CSA_ERR_TIMEOUT, K_FP8_PROJ, blockIdx.x, 3);
-                    break;
                 }
-                const int x = (b0 + (int)it) * PB;
-                tc::mbar_arrive_expect_tx(&full[st], C::W_BYTES + C::T_BYTES);
-                tc::tma_load_2d(sW + st * C::W_BYTES, &tmW, &full[st], x, grp * a.N + n0);
-                tc::tma_load_2d(sT + st * C::T_BYTES, &tmA, &full[st], grp * a.K + x, (int)t0);
+                break;
             }
-            volatile int never = 0;
-            for (uint32_t j = it > C::STAGES ? it - C::STAGES : 0; j < it; j++)
-                static_cast<void>(tc::mbar_wait(&full[j % C::STAGES], (j / C::STAGES) & 1, &never,
-                                                200000000ull));
+            uint64_t *landed = &full[it % C::FULLS];
+            if (warp == 0) {
+                if (tc::elect_one()) {
+                    const int x = (b0 + (int)it) * PB;
+                    tc::mbar_arrive_expect_tx(landed, C::W_BYTES + C::T_BYTES);
+                    tc::tma_load_2d(sW + st * C::W_BYTES, &tmW, landed, x, grp * a.N + n0);
+                    tc::tma_load_2d(sT + st * C::T_BYTES, &tmA, landed, grp * a.K + x, t0);
+                }
+                __syncwarp();
+            } else {
+                // zeros (from any valid address) behind the last token
+                float *slot = sS + it % C::SRING * C::SLOT;
+#pragma unroll
+                for (int i = 0; i < TT; i += 32)
+                    if (i + lane < TT)
+                        tc::cp_async4(slot + i + lane,
+                                      i + lane < rows ? as + (int64_t)i * a.las + it : a.As,
+                                      i + lane < rows ? 4 : 0);
+                if (lane == 0)
+                    tc::cp_async4(slot + TT, ws + it, 4);
+                tc::cp_async_arrive(landed);
+            }
         }
-    } else if (warp == 1) {
-        if (lane == 0) {
-            // ---------------- MMA issuer
-            constexpr uint32_t idesc = tc::idesc_e4m3(128, TT);
-            const uint32_t sWa = tc::smem_u32(sW), sTa = tc::smem_u32(sT);
-            for (uint32_t it = 0; it < nblk; it++) {
-                const int st = it % C::STAGES, buf = it % C::NBUF;
-                if ((it >= C::NBUF &&
-                     !tc::mbar_wait_sleep(&acce[buf], ((it / C::NBUF) - 1) & 1, abortv)) ||
-                    !tc::mbar_wait_sleep(&full[st], (it / C::STAGES) & 1, abortv)) {
+        // let the copies in flight land before the block exits
+        volatile int never = 0;
+        if (warp == 3)
+            tc::cp_async_wait_all();
+        else
+            for (uint32_t j = it > C::STAGES ? it - C::STAGES : 0; j < it; j++)
+                static_cast<void>(tc::mbar_wait(&full[j % C::FULLS], (j / C::FULLS) & 1, &never,
+                                                200000000ull));
+    } else if (warp < 3) {
+        // ---------------- MMA issuers
+        constexpr uint32_t idesc = tc::idesc_e4m3(128, TT);
+        const uint64_t dW = tc::sdesc_sw128(tc::smem_u32(sW)), dT = tc::sdesc_sw128(tc::smem_u32(sT));
+        for (uint32_t it = warp - 1; it < nblk; it += 2) {
+            const uint32_t st = it % C::STAGES, buf = it % C::NBUF;
+            const uint32_t pa = (it / C::NBUF - 1) & 1, pf = (it / C::FULLS) & 1;
+            uint64_t *landed = &full[it % C::FULLS];
+            const bool free = it < C::NBUF || tc::mbar_test_wait(&acce[buf], pa);
+            bool ok = tc::mbar_test_wait(landed, pf) || tc::mbar_wait_sleep(landed, pf, abortv);
+            ok = ok && (free || tc::mbar_wait_sleep(&acce[buf], pa, abortv));
+            if (!ok) {
+                if (lane == 0) {
                     *abort_flag = 1;
                     report(a.err, CSA_ERR_TIMEOUT, K_FP8_PROJ, blockIdx.x, 4);
-                    break;
                 }
-                tc::fence_after();
+                break;
+            }
+            tc::fence_after();
+            if (tc::elect_one()) {
+                const uint64_t dw = dW + ((st * C::W_BYTES) >> 4), dt = dT + ((st * C::T_BYTES) >> 4);
 #pragma unroll
                 for (int kk = 0; kk < PB / UK; kk++)
-                    tc::mma_f8(tmem + buf * TT, tc::sdesc_sw128(sWa + st * C::W_BYTES + kk * UK),
-                               tc::sdesc_sw128(sTa + st * C::T_BYTES + kk * UK), idesc, kk != 0);
+                    tc::mma_f8(tmem + buf * TT, dw + (kk * UK >> 4), dt + (kk * UK >> 4), idesc,
+                               kk != 0);
                 tc::mma_commit(&empty[st]);
                 tc::mma_commit(&accf[buf]);
             }
-            tc::mma_commit(done);
-            volatile int never = 0;
-            static_cast<void>(tc::mbar_wait(done, 0, &never, 200000000ull));
+            __syncwarp();
         }
+        __syncwarp();
+        if (tc::elect_one())
+            tc::mma_commit(done);
+        __syncwarp();
+        volatile int never = 0;
+        static_cast<void>(tc::mbar_wait(done, 0, &never, 200000000ull));
     } else {
         // ---------------- epilogue: feature n0 + 32 (warp % 4) + lane
         constexpr int CH = TT < 32 ? TT : 32;          // columns per load
-        constexpr int NS = (TT + 31) / 32;             // scales a lane brings
         const int q4 = warp & 3;
         const uint32_t lane_addr = tmem + ((uint32_t)(q4 * 32) << 16);
-        float *mine = sc + (warp - 2) * 2 * TT;
-        const float *ws = a.Ws + fb * a.nb;
-        auto scale_of = [&](int i, uint32_t it) {
-            const int64_t t = t0 + i * 32 + lane;
-            return it < nblk && t < a.M && i * 32 + lane < TT
-                       ? a.As[t * a.las + (int64_t)grp * a.nb + b0 + it] * ws[b0 + it]
-                       : 0.f;
-        };
-        float acc[TT], nxt[NS];
+        float2 acc[TT / 2];
 #pragma unroll
-        for (int j = 0; j < TT; j++)
-            acc[j] = 0.f;
-#pragma unroll
-        for (int i = 0; i < NS; i++)
-            nxt[i] = scale_of(i, 0);
+        for (int j = 0; j < TT / 2; j++)
+            acc[j] = make_float2(0.f, 0.f);
         for (uint32_t it = 0; it < nblk; it++) {
-            const int buf = it % C::NBUF;
-            float *cur = mine + (it & 1) * TT;
-#pragma unroll
-            for (int i = 0; i < NS; i++) {
-                if (TT >= 32 || lane < TT)
-                    cur[i * 32 + lane] = nxt[i];
-                nxt[i] = scale_of(i, it + 1);
-            }
-            __syncwarp();
+            const uint32_t buf = it % C::NBUF;
             if (!tc::mbar_wait_sleep(&accf[buf], (it / C::NBUF) & 1, abortv)) {
                 *abort_flag = 1;
                 report(a.err, CSA_ERR_TIMEOUT, K_FP8_PROJ, blockIdx.x, 5);
                 break;
             }
             tc::fence_after();
+            // landed before the MMAs of this block were let go
+            const float *slot = sS + it % C::SRING * C::SLOT;
+            const float2 w = make_float2(slot[TT], slot[TT]);
 #pragma unroll
             for (int c = 0; c < TT / CH; c++) {
                 uint32_t v[CH];
-                if constexpr (CH == 32)
-                    tc::tmem_ld32(lane_addr + buf * TT + c * CH, v);
-                else
-                    tc::tmem_ld16(lane_addr + buf * TT + c * CH, v);
-                tc::tmem_ld_wait(v);
+                tc::tmem_get(lane_addr + buf * TT + c * CH, v);
 #pragma unroll
                 for (int j = 0; j < CH; j += 4) {
-                    const float4 s = *(const float4 *)&cur[c * CH + j];
-                    acc[c * CH + j] = fmaf(__uint_as_float(v[j]), s.x, acc[c * CH + j]);
-                    acc[c * CH + j + 1] = fmaf(__uint_as_float(v[j + 1]), s.y, acc[c * CH + j + 1]);
-                    acc[c * CH + j + 2] = fmaf(__uint_as_float(v[j + 2]), s.z, acc[c * CH + j + 2]);
-                    acc[c * CH + j + 3] = fmaf(__uint_as_float(v[j + 3]), s.w, acc[c * CH + j + 3]);
+                    const float4 x = *(const float4 *)&slot[c * CH + j];
+                    float2 &lo = acc[(c * CH + j) / 2], &hi = acc[(c * CH + j) / 2 + 1];
+                    lo = __ffma2_rn(make_float2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])),
+                                    __fmul2_rn(make_float2(x.x, x.y), w), lo);
+                    hi = __ffma2_rn(
+                        make_float2(__uint_as_float(v[j + 2]), __uint_as_float(v[j + 3])),
+                        __fmul2_rn(make_float2(x.z, x.w), w), hi);
                 }
             }
             tc::fence_before();
@@ -580,10 +601,13 @@ proj_cols_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             if (lane == 0)
                 tc::mbar_arrive(&acce[buf]);
         }
-        // the last accumulator's commit covers every MMA: the ring is drained
+        // the last accumulator's commit covers every MMA of its issuer, the one
+        // before the other's: the ring is drained
 #pragma unroll
-        for (int j = 0; j < TT; j++)
-            partial[j * 128 + q4 * 32 + lane] = acc[j];
+        for (int j = 0; j < TT / 2; j++) {
+            partial[2 * j * 128 + q4 * 32 + lane] = acc[j].x;
+            partial[(2 * j + 1) * 128 + q4 * 32 + lane] = acc[j].y;
+        }
     }
     tc::fence_before();
     __syncthreads();
@@ -592,14 +616,21 @@ proj_cols_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     // token t0 + j, features n0 + 4 lane .. + 3
     const int nw = C::THREADS / 32;
     for (int j = rank + split * warp; j < TT && t0 + j < a.M; j += split * nw) {
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int p = 0; p < split; p++) {
-            const float *src = partial + j * 128 + lane * 4;
-            const float4 u = split > 1 ? tc::cluster_ld4(src, p) : *(const float4 *)src;
-            v.x += u.x;
-            v.y += u.y;
-            v.z += u.z;
-            v.w += u.w;
+        const float *src = partial + j * 128 + lane * 4;
+        float4 v;
+        if (split > 1) {
+            float4 u[kMaxSplit];                       // all in flight before the first is added
+#pragma unroll
+            for (int p = 0; p < kMaxSplit; p++)
+                if (p < split)
+                    u[p] = tc::cluster_ld4(src, p);
+            v = u[0];
+#pragma unroll
+            for (int p = 1; p < kMaxSplit; p++)
+                if (p < split)
+                    v = make_float4(v.x + u[p].x, v.y + u[p].y, v.z + u[p].z, v.w + u[p].w);
+        } else {
+            v = *(const float4 *)src;
         }
         const int cols = a.N - n0 - lane * 4;         // features of this lane that exist
         const int64_t t = t0 + j, o = t * a.ldo + (int64_t)grp * a.N + n0 + lane * 4;
@@ -645,6 +676,116 @@ proj_cols_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     if (warp == 1) {
         tc::fence_after();
         tc::tmem_dealloc(tmem, C::TMEM);
+    }
+}
+
+// ------------------------------------------------------------ very few tokens
+
+// Up to 8 tokens: the weight's bytes are all that counts, and what a call waits
+// for. A warp takes 16 features and a share of the input blocks: 16-byte loads
+// of the weight straight into the fragments of 16 x 8 x 32 warp MMAs (no tensor
+// memory to allocate, no ring to fill: one token by 1024 x 4096 takes 4.3 us in
+// a graph, against 5.9 us through the kernel above), the loads of four blocks
+// in flight before the first is used. Which inputs share an MMA does not matter
+// as long as both operands agree: lane (g, t) = (lane / 4, lane % 4) holds
+// inputs 16 t .. 16 t + 15 of every 64, eight for each of two MMAs, of features
+// g and g + 8 and of token g. A block of threads is rg groups of 16 features x
+// ks shares of the inputs, whose sums meet in shared memory in the order of the
+// shares.
+constexpr int kFewTokens = 8, kFewWarps = 16, kFewAhead = 4;
+constexpr int kFewLd = kFewTokens + 1;                // padded against bank conflicts
+
+__device__ __forceinline__ uint4 ld_stream(const uint8_t *p)
+{
+    uint4 v;
+    asm("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+        : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+        : "l"(p));
+    return v;
+}
+
+__device__ __forceinline__ void mma_16x8x32(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                            uint32_t a3, uint32_t b0, uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__global__ void __launch_bounds__(32 * kFewWarps)
+proj_few_kernel(const uint8_t *__restrict__ A, const uint8_t *__restrict__ W, const ProjDev a,
+                const int ks)
+{
+    extern __shared__ float sums[];                   // [ks][16 rg][kFewLd]
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int rg = blockDim.x / 32 / ks, share = warp / rg, group = warp % rg;
+    const int rows = 16 * rg;                         // features of the block
+    const int ft = (a.N + rows - 1) / rows;
+    const int grp = blockIdx.x / ft, n0 = blockIdx.x % ft * rows;
+    const int f0 = n0 + 16 * group;                   // the warp's first feature, in its group
+    const int b0 = (int)((int64_t)a.nb * share / ks), b1 = (int)((int64_t)a.nb * (share + 1) / ks);
+    const int M = (int)a.M;
+    const bool r0 = f0 + g < a.N, r1 = f0 + g + 8 < a.N, tok = g < M;
+    const uint8_t *w0 = W + ((int64_t)grp * a.N + (r0 ? f0 + g : 0)) * a.K;
+    const uint8_t *w1 = W + ((int64_t)grp * a.N + (r1 ? f0 + g + 8 : 0)) * a.K;
+    const uint8_t *x0 = A + ((int64_t)(tok ? g : 0) * a.groups + grp) * a.K;
+    const float *as = a.As + (int64_t)grp * a.nb;
+    const float *ws = a.Ws + ((int64_t)grp * a.N + (f0 < a.N ? f0 : 0)) / PB * a.nb;
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};              // (feature g + 8 (e / 2), token 2 t + e % 2)
+    for (int b = b0; b < b1; b += kFewAhead) {
+        uint4 wa[kFewAhead][2], wb[kFewAhead][2];
+        float sw[kFewAhead], sa[kFewAhead][2];
+#pragma unroll
+        for (int i = 0; i < kFewAhead; i++) {
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                const int k = (b + i) * PB + h * 64 + t * 16;
+                const bool in = b + i < b1 && k < a.K;
+                wa[i][h] = in && r0 ? ld_stream(w0 + k) : zero;
+                wb[i][h] = in && r1 ? ld_stream(w1 + k) : zero;
+            }
+            sw[i] = b + i < b1 ? ws[b + i] : 0.f;
+#pragma unroll
+            for (int e = 0; e < 2; e++)
+                sa[i][e] =
+                    b + i < b1 && 2 * t + e < M ? as[(int64_t)(2 * t + e) * a.las + b + i] : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < kFewAhead; i++) {
+            if (b + i >= b1)
+                break;
+            float p[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                const int k = (b + i) * PB + h * 64 + t * 16;
+                const uint4 x = tok && k < a.K ? __ldg((const uint4 *)(x0 + k)) : zero;
+                mma_16x8x32(p, wa[i][h].x, wb[i][h].x, wa[i][h].y, wb[i][h].y, x.x, x.y);
+                mma_16x8x32(p, wa[i][h].z, wb[i][h].z, wa[i][h].w, wb[i][h].w, x.z, x.w);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; e++)
+                acc[e] = fmaf(p[e], sa[i][e & 1] * sw[i], acc[e]);
+        }
+    }
+    float *mine = sums + (share * rows + 16 * group) * kFewLd;
+#pragma unroll
+    for (int e = 0; e < 4; e++)
+        mine[(g + 8 * (e >> 1)) * kFewLd + 2 * t + (e & 1)] = acc[e];
+    __syncthreads();
+    for (int i = threadIdx.x; i < rows * M; i += blockDim.x) {
+        const int m = i / rows, f = i - m * rows;
+        if (n0 + f >= a.N)
+            continue;
+        float v = 0.f;
+        for (int q = 0; q < ks; q++)
+            v += sums[(q * rows + f) * kFewLd + m];
+        const int64_t o = m * a.ldo + (int64_t)grp * a.N + n0 + f;
+        if (a.out_dt == CSA_BF16)
+            ((__nv_bfloat16 *)a.out)[o] = __float2bfloat16_rn(v);
+        else
+            ((float *)a.out)[o] = v;
     }
 }
 
@@ -705,8 +846,10 @@ cudaError_t launch_cols(const Fp8ProjArgs &g, ProjDev d, int sms, cudaStream_t s
     if (e != cudaSuccess)
         return e;
     const int64_t tiles = (g.M + TT - 1) / TT * ((g.N + 127) / 128) * g.groups;
+    if (tiles > INT32_MAX / kMaxSplit)
+        return cudaErrorInvalidConfiguration;
     int split = 1;
-    while (split < 8 && tiles * split * 2 <= sms && split * 2 <= d.nb)
+    while (split < kMaxSplit && tiles * split * 2 <= sms && split * 2 <= d.nb)
         split *= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(tiles * split));
@@ -719,6 +862,20 @@ cudaError_t launch_cols(const Fp8ProjArgs &g, ProjDev d, int sms, cudaStream_t s
     cfg.attrs = at;
     cfg.numAttrs = split > 1 ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, proj_cols_kernel<TT>, tmA, tmW, d, split);
+}
+
+cudaError_t launch_few(const Fp8ProjArgs &g, const ProjDev &d, int sms, cudaStream_t s)
+{
+    // shares of the inputs until every SM has eight warps
+    const int64_t tiles = (int64_t)g.groups * ((g.N + 15) / 16);
+    int ks = 1;
+    while (ks < kFewWarps && 2 * ks <= d.nb && tiles * ks < 8 * (int64_t)sms)
+        ks *= 2;
+    const int rg = ks >= 8 ? 1 : 8 / ks;
+    const int64_t blocks = (int64_t)g.groups * ((g.N + 16 * rg - 1) / (16 * rg));
+    proj_few_kernel<<<(unsigned)blocks, 32 * rg * ks, ks * 16 * rg * kFewLd * 4, s>>>(g.A, g.W, d,
+                                                                                      ks);
+    return cudaGetLastError();
 }
 
 }  // namespace
@@ -744,14 +901,24 @@ cudaError_t launch_fp8_proj(const Fp8ProjArgs &g, unsigned *err, cudaStream_t s)
     const int sms = sm_count();
     // 128 x 128 tiles that the call has
     const int64_t tiles = (g.M + 127) / 128 * ((g.N + 127) / 128) * g.groups;
+    // Up to 8 tokens take the kernel that waits least, but for e4m3 results (a
+    // scale's 128 features would have to share a block) and for weights of many
+    // short rows, which the ring streams better (8 tokens by 32768 x 1024: 9.7
+    // against 10.6 us; by 16384 x 4096: 19.1 against 18.4 us).
+    const int64_t few_tiles = (int64_t)g.groups * ((g.N + 15) / 16);
+    if (g.M <= kFewTokens && g.out_dt != CSA_E4M3 && (d.nb >= 16 || few_tiles < 8 * (int64_t)sms))
+        return launch_few(g, d, sms, s);
     if (g.M <= 16)
         return launch_cols<16>(g, d, sms, s);
     if (g.M <= 32)
         return launch_cols<32>(g, d, sms, s);
-    if (g.M <= 64)
+    // More tokens take the row kernel, unless its tiles would leave half the SMs
+    // idle over long rows, which a cluster shares (333 tokens by 1000 x 2064:
+    // 9.3 against 11.1 us; 128 by 1024 x 4096: 9.2 against 12.1; but 100 by 8192
+    // x 1024: 7.7 against 6.0).
+    const int64_t cols_tiles = (g.M + 63) / 64 * ((g.N + 127) / 128) * g.groups;
+    if (d.nb >= 16 && 2 * cols_tiles <= sms)
         return launch_cols<64>(g, d, sms, s);
-    if (2 * tiles <= sms)
-        return launch_cols<128>(g, d, sms, s);
     if (tiles <= 2 * sms)
         return launch_rows<128>(g, d, sms, s);
     return launch_rows<256>(g, d, sms, s);
