@@ -14,6 +14,7 @@
 #include "common.cuh"
 #include "kernels.h"
 #include "quant8.cuh"
+#include "tc.cuh"
 
 namespace csa {
 
@@ -104,12 +105,11 @@ __device__ __forceinline__ void load_gains(const float *gamma, int j, bool align
     }
 }
 
-// Sum over a row's tpr threads (a multiple of 32); `part` is this call's own
-// place of 32 floats. Threads of other rows of the block take part as well.
+// Sum over a row's tpr threads: 8, 16 or a multiple of 32. `part` is this
+// call's own place of 32 floats. Threads of other rows take part as well.
 __device__ __forceinline__ float row_sum(float ss, int tpr, int sub, float *part)
 {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
+    for (int o = min(tpr, 32) >> 1; o > 0; o >>= 1)
         ss += __shfl_xor_sync(0xffffffffu, ss, o);
     if (tpr > 32) {
         const int w0 = (threadIdx.x - sub) >> 5;
@@ -143,26 +143,30 @@ __device__ __forceinline__ void write_piece(const float2 (&v)[kPairs], bool live
     }
 }
 
-// Rows of up to 16 tpr values, tpr threads (a multiple of 32) to a row and
-// blockDim / tpr rows at a time; the grid is resident and strides over the
-// rows. A thread's 16 values stay in its registers from the one read to the
-// outputs, so that each byte crosses HBM once and only the sum of squares is
-// exchanged, and its 16 gains for all its rows (read per row they cost more L1
-// traffic than the row). In bf16 the next row is read while this one is
-// written.
-template <typename T>
-__global__ void __launch_bounds__(512, sizeof(T) == 2 ? 2 : 1)
+// Rows of up to 16 tpr values, tpr threads to a row and blockDim / tpr rows at
+// a time; the grid is resident and strides over the rows. A thread's 16 values
+// stay in its registers from the one read to the outputs, so that each byte
+// crosses HBM once and only the sum of squares is exchanged, and its 16 gains
+// for all its rows (read per row they cost more L1 traffic than the row). In
+// bf16 the next row is read while this one is written.
+// A few longer rows are each cut over a cluster of thread blocks (CLUSTER; `cut`
+// values a block), which add their sums of squares in the order of their ranks:
+// one row of 32768 takes 4.7 us in a graph, read twice by one block 9.2 us.
+template <typename T, bool CLUSTER, int MOST>
+__global__ void __launch_bounds__(MOST, sizeof(T) == 2 && MOST == 512 ? 2 : 1)
 add_norm_quant_kernel(const T *x, const T *residual, const float *__restrict__ gamma,
-                      bool gamma_aligned, int64_t rows, int d, int tpr, float eps, T *total, T *y,
-                      uint8_t *codes, float *scale)
+                      bool gamma_aligned, int64_t rows, int d, int tpr, int cut, int ranks,
+                      float eps, T *total, T *y, uint8_t *codes, float *scale)
 {
     constexpr bool kAhead = sizeof(T) == 2;
     __shared__ float part[2][32];
+    __shared__ float sums[2];
+    const int rank = CLUSTER ? (int)tc::cluster_rank() : 0;
     const int sub = threadIdx.x % tpr;
     const int rpb = blockDim.x / tpr;
-    const int j = sub * kLane;
+    const int j = rank * cut + sub * kLane;
     const int nb = (d + kBlock - 1) / kBlock;
-    const bool in = j < d;
+    const bool in = j < d && sub * kLane < cut;
     float2 g[kPairs];
 #pragma unroll
     for (int e = 0; e < kPairs; e++)
@@ -170,8 +174,8 @@ add_norm_quant_kernel(const T *x, const T *residual, const float *__restrict__ g
     if (gamma && in)
         load_gains(gamma, j, gamma_aligned, g);
     Raw<T> a, b;
-    int64_t r0 = (int64_t)blockIdx.x * rpb;           // the block's first row
-    const int64_t stride = (int64_t)gridDim.x * rpb, mine = threadIdx.x / tpr;
+    const int64_t stride = (int64_t)gridDim.x / ranks * rpb, mine = threadIdx.x / tpr;
+    int64_t r0 = (int64_t)(blockIdx.x / ranks) * rpb;  // the block's first row
     auto read = [&](int64_t row) {
         if (row < rows && in) {
             a.load(x + row * d + j);
@@ -199,16 +203,34 @@ add_norm_quant_kernel(const T *x, const T *residual, const float *__restrict__ g
             read(row + stride);
         if (live && total)
             store_16(total + base + j, v);
-        const float ss = row_sum(ss2.x + ss2.y, tpr, sub, part[parity]);
+        float ss = row_sum(ss2.x + ss2.y, tpr, sub, part[parity]);
+        if (CLUSTER) {
+            // the place of one row is written again two rows later, when every
+            // block has passed the next row's barrier and so read this one
+            if (threadIdx.x == 0)
+                sums[parity] = ss;
+            __syncwarp();
+            tc::cluster_sync();
+            ss = 0.f;
+            for (int q = 0; q < ranks; q++)
+                ss += tc::cluster_ld(&sums[parity], q);
+        }
         const float inv = 1.f / sqrtf(ss / d + eps);
 #pragma unroll
         for (int e = 0; e < kPairs; e++)
             v[e] = __fmul2_rn(__fmul2_rn(v[e], make_float2(inv, inv)), g[e]);
         write_piece(v, live, base, j, row, nb, y, codes, scale);
     }
+    if (CLUSTER) {
+        // no block leaves while another may still read its sums
+        __syncwarp();
+        tc::cluster_sync();
+    }
 }
 
-// Longer rows, one to a block, read a second time (from L2) for the outputs.
+// Many rows too long for a block's registers, one to a block, are read a second
+// time (from L2) for the outputs; the cluster's barrier a row would cost more
+// (4096 rows of 32768: 339 against 214 us).
 constexpr int kLongThreads = 512;
 
 template <typename T>
@@ -217,36 +239,42 @@ add_norm_quant_long_kernel(const T *x, const T *residual, const float *__restric
                            bool gamma_aligned, int d, float eps, T *total, T *y, uint8_t *codes,
                            float *scale)
 {
+    constexpr int kStep = kLongThreads * kLane;
     __shared__ float part[32];
     const int64_t row = blockIdx.x, base = row * d;
     const int nb = (d + kBlock - 1) / kBlock;
-    float2 v[kPairs];
+    const int first = threadIdx.x * kLane;
+    Raw<T> a, b;
     auto read = [&](int j) {
-        Raw<T> a, b;
         if (j < d) {
             a.load(x + base + j);
             if (residual)
                 b.load(residual + base + j);
         }
+    };
+    // the piece read last, and the next one on its way
+    float2 v[kPairs], ss2 = make_float2(0.f, 0.f);
+    auto take = [&](int j) {
 #pragma unroll
         for (int e = 0; e < kPairs; e++) {
             v[e] = make_float2(0.f, 0.f);
             if (j < d)
                 v[e] = residual ? __fadd2_rn(a.pair(e), b.pair(e)) : a.pair(e);
         }
+        read(j + kStep);
     };
-    float2 ss2 = make_float2(0.f, 0.f);
-    for (int j0 = 0; j0 < d; j0 += kLongThreads * kLane) {
-        read(j0 + threadIdx.x * kLane);
+    read(first);
+    for (int j = first; j - first < d; j += kStep) {
+        take(j);
 #pragma unroll
         for (int e = 0; e < kPairs; e++)
             ss2 = __ffma2_rn(v[e], v[e], ss2);
     }
+    read(first);
     const float ss = row_sum(ss2.x + ss2.y, kLongThreads, threadIdx.x, part);
     const float inv = 1.f / sqrtf(ss / d + eps);
-    for (int j0 = 0; j0 < d; j0 += kLongThreads * kLane) {
-        const int j = j0 + threadIdx.x * kLane;
-        read(j);
+    for (int j = first; j - first < d; j += kStep) {
+        take(j);
         if (j < d && total)
             store_16(total + base + j, v);
 #pragma unroll
@@ -398,32 +426,64 @@ cudaError_t launch_quant(const AddNormQuantArgs &a, cudaStream_t s)
     return cudaGetLastError();
 }
 
+template <typename T, bool CLUSTER, int MOST>
+cudaError_t launch_norm(const AddNormQuantArgs &a, int tpr, int rpb, int cut, int ranks,
+                        cudaStream_t s)
+{
+    int dev = 0, sms = 148, per_sm = 1;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(
+        &per_sm, add_norm_quant_kernel<T, CLUSTER, MOST>, tpr * rpb, 0);
+    if (e != cudaSuccess)
+        return e;
+    const int64_t want = (a.rows + rpb - 1) / rpb, room = (int64_t)sms * per_sm / ranks;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((want < room ? want : room) * ranks));
+    cfg.blockDim = dim3(tpr * rpb);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim = {(unsigned)ranks, 1, 1};
+    cfg.attrs = at;
+    cfg.numAttrs = CLUSTER ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, add_norm_quant_kernel<T, CLUSTER, MOST>, (const T *)a.x,
+                              (const T *)a.residual, a.gamma, ((uintptr_t)a.gamma & 15u) == 0,
+                              a.rows, a.d, tpr, cut, ranks, a.eps, (T *)a.total, (T *)a.y,
+                              a.codes, a.scale);
+}
+
 template <typename T>
 cudaError_t launch_add_norm_quant_t(const AddNormQuantArgs &a, cudaStream_t s)
 {
     if (!a.normalise)
         return a.d % kBlock == 0 ? launch_quant<T, true>(a, s) : launch_quant<T, false>(a, s);
-    const bool ga = ((uintptr_t)a.gamma & 15u) == 0;
-    const int warps = (a.d + 32 * kLane - 1) / (32 * kLane);
-    if (warps * 32 > 512) {
-        add_norm_quant_long_kernel<T><<<(unsigned)a.rows, kLongThreads, 0, s>>>(
-            (const T *)a.x, (const T *)a.residual, a.gamma, ga, a.d, a.eps, (T *)a.total,
-            (T *)a.y, a.codes, a.scale);
-        return cudaGetLastError();
+    const int pieces = a.d / kLane;
+    if (pieces <= 512) {
+        const int tpr = pieces <= 8 ? 8 : pieces <= 16 ? 16 : (pieces + 31) / 32 * 32;
+        return launch_norm<T, false, 512>(a, tpr, tpr <= 256 ? 256 / tpr : 1, a.d, 1, s);
     }
-    const int tpr = 32 * warps, rpb = warps <= 8 ? 8 / warps : 1;
-    int dev = 0, sms = 148, per_sm = 1;
+    // whole scale blocks to each thread block of the cluster, 4096 values at a
+    // time as long as eight blocks suffice
+    const int nb = (a.d + kBlock - 1) / kBlock;
+    int ranks = 2;
+    while (ranks < 8 && (nb + ranks - 1) / ranks > 32)
+        ranks *= 2;
+    int dev = 0, sms = 148;
     cudaGetDevice(&dev);
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(
-        &per_sm, add_norm_quant_kernel<T>, tpr * rpb, 0);
-    if (e != cudaSuccess)
-        return e;
-    const int64_t want = (a.rows + rpb - 1) / rpb, room = (int64_t)sms * per_sm;
-    add_norm_quant_kernel<T><<<(unsigned)(want < room ? want : room), tpr * rpb, 0, s>>>(
-        (const T *)a.x, (const T *)a.residual, a.gamma, ga, a.rows, a.d, tpr, a.eps,
-        (T *)a.total, (T *)a.y, a.codes, a.scale);
-    return cudaGetLastError();
+    if (a.rows * ranks > sms) {
+        if constexpr (sizeof(T) == 2)                 // float32 would spill
+            if (pieces <= 1024)
+                return launch_norm<T, false, 1024>(a, (pieces + 31) / 32 * 32, 1, a.d, 1, s);
+        add_norm_quant_long_kernel<T><<<(unsigned)a.rows, kLongThreads, 0, s>>>(
+            (const T *)a.x, (const T *)a.residual, a.gamma, ((uintptr_t)a.gamma & 15u) == 0, a.d,
+            a.eps, (T *)a.total, (T *)a.y, a.codes, a.scale);
+        return cudaGetLastError();
+    }
+    const int blocks = (nb + ranks - 1) / ranks;
+    return launch_norm<T, true, 512>(a, (blocks * (kBlock / kLane) + 31) / 32 * 32, 1, blocks * kBlock,
+                                ranks, s);
 }
 
 }  // namespace

@@ -411,7 +411,8 @@ __device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[16])
 
 // Rank of this block in its cluster; the hardware barrier over all threads of
 // the cluster (every thread of every block reaches it; a warp's threads
-// together); 16 bytes of another block's shared memory at the place of `local`.
+// together); 4 or 16 bytes of another block's shared memory at the place of
+// `local`.
 __device__ __forceinline__ uint32_t cluster_rank()
 {
     uint32_t r;
@@ -423,6 +424,15 @@ __device__ __forceinline__ void cluster_sync()
 {
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ float cluster_ld(const float *local, uint32_t rank)
+{
+    uint32_t ra;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(ra) : "r"(smem_u32(local)), "r"(rank));
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(ra) : "memory");
+    return v;
 }
 
 __device__ __forceinline__ float4 cluster_ld4(const void *local, uint32_t rank)

@@ -11,6 +11,12 @@ outputs in device memory and run one pass of the path per ``step()``:
 * decode: indexer scores -> top-k -> sparse attention, and HCA dense
   attention, for a batch of single-token queries over long caches.
 
+``Projections8`` brings hidden states to these operands with 8-bit products
+(residual addition, RMSNorm and e4m3 storage in one call, then block-scaled
+e4m3 projections), for prompts and for single tokens alike; ``CsaLayer8`` is a
+whole CSA layer: the projections, a CSA prefill, and the grouped output
+projection in 8 bits.
+
 Only buffer management and argument marshalling live here; every step runs
 in ``libcsa.so``. The raw window KV of a prefill is the pre-compression KV
 (C^a for CSA, C for HCA).
@@ -381,6 +387,141 @@ class Decode:
 
     def result(self):
         return self.out
+
+    def step(self, stream=None):
+        for _, f in self.phases():
+            f(stream)
+
+
+def _store_weight(W, device):
+    """(codes, scale) of an [out, in] weight, as csa_fp8_proj reads it."""
+    W = W.to(device).contiguous()
+    N, K = W.shape
+    codes = torch.empty(N, K, device=device, dtype=torch.float8_e4m3fn)
+    scale = torch.empty(-(-N // 128), -(-K // 128), device=device, dtype=torch.float32)
+    abi.csa_quantize_weight(W, codes, scale)
+    return codes, scale
+
+
+def _e4m3_rows(n, d, device):
+    return (torch.empty(n, d, device=device, dtype=torch.float8_e4m3fn),
+            torch.empty(n, -(-d // 128), device=device, dtype=torch.float32))
+
+
+class Projections8:
+    """The projections of a CSA layer (Module B steps 1-3) in 8 bits, for n
+    tokens at a time: C^a .. Z^b and the indexer-key compressor's operands, w^I
+    (float32), and through the latent c^Q (kept in e4m3) q and q^I. Weights are
+    stored in e4m3 once, from the [in, out] matrices of
+    ``workloads.layer_draws``. For an e4m3 indexer (head width 128) q^I leaves
+    its product as codes with a scale for each head, which is what the indexer
+    reads. The outputs (``ops``) have the keys and shapes of
+    ``workloads.csa_operands``."""
+
+    FROM_H = (("Ca", "W_aKV"), ("Cb", "W_bKV"), ("Za", "W_aZ"), ("Zb", "W_bZ"),
+              ("CIa", "W_aKI"), ("CIb", "W_bKI"), ("ZIa", "W_aZI"), ("ZIb", "W_bZI"))
+
+    def __init__(self, w, weights: Dict[str, torch.Tensor], n: Optional[int] = None,
+                 device="cuda"):
+        if w.dtype != "bf16" or w.idx_dtype not in ("bf16", "e4m3"):
+            raise ValueError("8-bit projections write bf16 operands and a bf16 or e4m3 indexer's")
+        if w.idx_dtype == "e4m3" and w.cI != 128:
+            raise ValueError("e4m3 indexer queries need head width 128 (a scale per 128 columns)")
+        self.w, self.n = w, w.n if n is None else n
+        self.W = {nm: _store_weight(weights[nm].t(), device)
+                  for nm in [b for _, b in self.FROM_H] + ["W_DQ", "W_w", "W_IUQ", "W_UQ"]}
+        n, d, dc = self.n, self.W["W_DQ"][0].shape[1], self.W["W_DQ"][0].shape[0]
+        self.h8, self.cq8 = _e4m3_rows(n, d, device), _e4m3_rows(n, dc, device)
+        bf = dict(device=device, dtype=torch.bfloat16)
+        self.ops = {nm: torch.empty(n, w.c if i < 4 else w.cI, **bf)
+                    for i, (nm, _) in enumerate(self.FROM_H)}
+        self.ops["wI"] = torch.empty(n, w.hI, device=device, dtype=torch.float32)
+        self.ops["q"] = torch.empty(n, w.h, w.c, **bf)
+        if w.idx_dtype == "e4m3":
+            self.ops["qI"] = torch.empty(n, w.hI, w.cI, device=device, dtype=torch.float8_e4m3fn)
+            self.ops["qI_scale"] = torch.empty(n, w.hI, device=device, dtype=torch.float32)
+        else:
+            self.ops["qI"] = torch.empty(n, w.hI, w.cI, **bf)
+
+    launches_per_step = 13
+
+    def normalise(self, x, residual=None, gamma=None, total=None, stream=None):
+        """x (+ residual) [n, d] normed into e4m3; total <- x + residual."""
+        abi.csa_add_norm_quant(x, residual, gamma, total=total, codes=self.h8[0],
+                               scale=self.h8[1], stream=stream)
+
+    def project_h(self, stream=None):
+        for nm, wn in self.FROM_H:
+            abi.csa_fp8_proj(*self.h8, *self.W[wn], self.ops[nm], stream=stream)
+        abi.csa_fp8_proj(*self.h8, *self.W["W_w"], self.ops["wI"], stream=stream)
+        abi.csa_fp8_proj(*self.h8, *self.W["W_DQ"], *self.cq8, stream=stream)
+
+    def project_q(self, stream=None):
+        n, o = self.n, self.ops
+        abi.csa_fp8_proj(*self.cq8, *self.W["W_UQ"], o["q"].view(n, -1), stream=stream)
+        abi.csa_fp8_proj(*self.cq8, *self.W["W_IUQ"], o["qI"].view(n, -1), o.get("qI_scale"),
+                         stream=stream)
+
+    def step(self, x, residual=None, gamma=None, total=None, stream=None):
+        self.normalise(x, residual, gamma, total, stream)
+        self.project_h(stream)
+        self.project_q(stream)
+
+
+class CsaLayer8:
+    """One causal CSA layer of a single sequence from its hidden states x [n, d]
+    (bf16): residual addition and RMSNorm, the 8-bit projections, the CSA
+    prefill (``CsaPrefill``: entries, keys, selection, attention) and, when
+    `Wg` [g d_g, h c / g] and `Wo` [d, g d_g] are given, the grouped output
+    projection with e4m3 heads and intermediate. `weights` as for
+    ``Projections8``, with the biases Ba, Bb, BIa, BIb and the sink."""
+
+    kind = "csa_layer8"
+
+    def __init__(self, w, x, weights: Dict[str, torch.Tensor], residual=None, gamma=None,
+                 Wg=None, Wo=None, g: int = 1, rope_dims: int = 0, fused: bool = False,
+                 device="cuda"):
+        self.w, self.g = w, g
+        self.x = x.to(device).contiguous()
+        self.residual = residual.to(device).contiguous() if residual is not None else None
+        self.gamma = gamma.to(device).contiguous() if gamma is not None else None
+        self.total = torch.empty_like(self.x) if residual is not None else None
+        self.proj = Projections8(w, weights, device=device)
+        ops = dict(self.proj.ops)
+        for nm in ("Ba", "Bb", "BIa", "BIb", "sink"):
+            ops[nm] = weights[nm].to(device=device, dtype=torch.float32)
+        self.core = CsaPrefill(w, ops, device=device, rope_dims=rope_dims, fused=fused)
+        self.out = None
+        if Wg is not None:
+            self.Wg, self.Wo = _store_weight(Wg, device), _store_weight(Wo, device)
+            self.o8 = _e4m3_rows(w.n, w.h * w.c, device)
+            self.u8 = _e4m3_rows(w.n, Wg.shape[0], device)
+            self.out = torch.empty(w.n, Wo.shape[0], device=device, dtype=torch.bfloat16)
+
+    @property
+    def launches_per_step(self):
+        return (self.proj.launches_per_step + self.core.launches_per_step
+                + (3 if self.out is not None else 0))
+
+    def normalise(self, stream=None):
+        self.proj.normalise(self.x, self.residual, self.gamma, self.total, stream)
+
+    def project_out(self, stream=None):
+        abi.csa_add_norm_quant(self.core.out.view(self.w.n, -1), normalise=False,
+                               codes=self.o8[0], scale=self.o8[1], stream=stream)
+        abi.csa_fp8_proj(*self.o8, *self.Wg, *self.u8, groups=self.g, stream=stream)
+        abi.csa_fp8_proj(*self.u8, *self.Wo, self.out, stream=stream)
+
+    def phases(self):
+        ph = [("norm_quant", self.normalise), ("proj_h", self.proj.project_h),
+              ("proj_q", self.proj.project_q)] + self.core.phases()
+        return ph + ([("proj_out", self.project_out)] if self.out is not None else [])
+
+    def inputs(self):
+        return {k: v for k, v in (("x", self.x), ("residual", self.residual)) if v is not None}
+
+    def result(self):
+        return self.core.out if self.out is None else self.out
 
     def step(self, stream=None):
         for _, f in self.phases():

@@ -69,6 +69,17 @@ NORM_CASES = [
     (2, 65520, torch.bfloat16, True, True, True),
     (1000, 64, torch.bfloat16, True, False, False),
     (129, 256, torch.float32, False, False, False),
+    # many rows longer than a block's threads hold at once
+    (200, 9216, torch.bfloat16, True, True, True),
+    (170, 16400, torch.bfloat16, False, True, True),
+    (160, 8208, torch.float32, True, False, True),
+    # one long row over a cluster whose last block is short
+    (1, 16640, torch.float32, True, True, True),
+    (3, 8336, torch.bfloat16, True, True, True),
+    # rows that share a warp
+    (70, 80, torch.bfloat16, True, True, True),
+    (131, 128, torch.float32, False, True, True),
+    (3000, 240, torch.bfloat16, True, True, True),
 ]
 
 
