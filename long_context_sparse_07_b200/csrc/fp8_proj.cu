@@ -51,50 +51,61 @@ __device__ __forceinline__ uint32_t bf16_2(float a, float b)
 
 // ------------------------------------------------------------ many tokens
 
-// Tiles of 128 tokens x TN features. Warp 0 issues the TMA loads, warps 1 and
-// 2 in turn the MMAs of a block, warp 3 copies the scales, TN / 16 epilogue
-// warps each own a TMEM lane quarter (32 tokens) and 64 features. Tensor memory
-// holds 512 / TN accumulators of one block each.
+// Tiles of 128 tokens x 128 features, or (PAIR) of 256 x 256 by two thread
+// blocks whose tensor cores work as one: a block brings 128 tokens and 128 of
+// the features, and holds the sums of its tokens and all features. Warp 0 issues
+// the TMA loads, warps 1 and 2 (of the leader) in turn the MMAs of a block of
+// inputs, warp 3 copies the scales, TN / 16 epilogue warps each own a TMEM lane
+// quarter (32 tokens) and 64 features. Tensor memory holds 512 / TN accumulators
+// of one block each.
+// A pair, because one block's tile of 128 x 256 is bound by shared memory: per
+// block of inputs the loads write 48 KB and the MMAs read 48 KB, 750 cycles at
+// 128 bytes a cycle where the MMAs take 512; in a pair it is 32 and 32 KB.
 // Two issuers, because an issuer goes on only when its last MMA has started,
 // and then needs some 450 cycles for its next barriers and issues, which the
-// other's MMAs (512 cycles a block at TN = 256) hide. Sixteen epilogue warps
-// with 64 sums a thread, because eight with 128 could not overlap their loads
-// from tensor memory (about 300 cycles of its port a block) with their sums
-// (256 cycles of the FMA pipe) and took 1050 cycles a block. With TN = 256 the
-// epilogue's threads take registers over from the first warpgroup (32 + 4 x 112
-// = 5 x 96). Scales are copied to shared memory as far ahead as the operands
-// (read by the epilogue itself, or by a warp that loads and then stores them,
-// their latency was the pace: 1000 cycles a block). Results leave through
+// other's MMAs hide. Sixteen epilogue warps with 64 sums a thread, because eight
+// with 128 could not overlap their loads from tensor memory (about 300 cycles
+// of its port a block) with their sums (256 cycles of the FMA pipe) and took
+// 1050 cycles a block; they take registers over from the first warpgroup (32 +
+// 4 x 112 = 5 x 96). Scales are copied to shared memory as far ahead as the
+// operands (read by the epilogue itself, or by a warp that loads and then stores
+// them, their latency was the pace: 1000 cycles a block). Results leave through
 // shared memory by TMA stores that run beside the next tile's products (stored
 // from the registers, 32 rows to a store instruction, a tile's results held its
 // epilogue for 6400 cycles, as long as seven blocks of inputs).
-template <int TN> struct Rows {
-    static constexpr int STAGES = TN == 256 ? 3 : 5;
-    static constexpr int NBUF = 512 / TN;
+template <bool PAIR> struct Rows {
+    static constexpr int TN = PAIR ? 256 : 128;       // features of a tile
+    static constexpr int TM = PAIR ? 256 : 128;       // tokens of a tile
+    static constexpr int STAGES = PAIR ? 4 : 5;
+    static constexpr int UPB = TN / 128;              // units of TM x 128 of a block
+    static constexpr int NBUF = 4;                    // units that tensor memory holds
     // Barriers of landed blocks: twice the stages. An issuer sees every second
     // block only, and a wait tells a barrier's phases apart by their parity, so
     // that each barrier has to have the same issuer for good.
     static constexpr int FULLS = 2 * STAGES;
-    static constexpr int EPI = TN / 16;
+    static constexpr int CW = PAIR ? 128 : 64;        // features of an epilogue warp
+    static constexpr int EPI = 4 * TN / CW;
     static constexpr int THREADS = 128 + 32 * EPI;
-    static constexpr uint32_t A_BYTES = 128 * PB, B_BYTES = TN * PB;
-    static constexpr uint32_t OUT_BYTES = 4096;       // of each epilogue warp: a store box
+    static constexpr uint32_t A_BYTES = 128 * PB, B_BYTES = 128 * PB;   // of each block
+    static constexpr int UROWS = 128 / UPB;           // features a block brings to a unit
+    static constexpr uint32_t OUT_BYTES = 64 * CW;    // of each epilogue warp: store boxes
     // scales of a block: when those of block it are copied, its ring stage is
     // free, so block it - STAGES is multiplied, which took the buffer of the
-    // block NBUF earlier, which therefore is drained
-    static constexpr int SRING = TN == 256 ? 8 : 16;
-    static_assert(SRING >= STAGES + NBUF, "scales are overwritten only after their use");
+    // block NBUF / UPB earlier, which therefore is drained
+    static constexpr int SRING = PAIR ? 8 : 16;
+    static_assert(SRING >= STAGES + NBUF / UPB, "scales are overwritten only after their use");
     static constexpr int SLOT = 128 + 4;              // 128 tokens', the features' blocks'
     static constexpr size_t SMEM = 1024 + STAGES * (A_BYTES + B_BYTES) + EPI * OUT_BYTES +
                                    SRING * SLOT * 4 + EPI * 32 * 4 + 512;
 };
 
-template <int TN>
-__global__ void __launch_bounds__(Rows<TN>::THREADS, 1)
+template <bool PAIR>
+__global__ void __launch_bounds__(Rows<PAIR>::THREADS, 1)
 proj_rows_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmW,
                  const __grid_constant__ CUtensorMap tmO, const ProjDev a)
 {
-    using R = Rows<TN>;
+    using R = Rows<PAIR>;
+    constexpr int TN = R::TN;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     uint8_t *sA = sm;
@@ -104,21 +115,30 @@ proj_rows_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     float *sM = sS + R::SRING * R::SLOT;                    // largest magnitudes [epilogue warp][32]
     uint64_t *full = (uint64_t *)(sM + R::EPI * 32), *empty = full + R::FULLS;
     uint64_t *accf = empty + R::STAGES, *acce = accf + R::NBUF, *done = acce + R::NBUF;
-    uint32_t *tmem_slot = (uint32_t *)(done + 1);
+    uint64_t *scaled = done + 1;                      // the second block's scales landed
+    uint32_t *tmem_slot = (uint32_t *)(scaled + R::SRING);
     int *abort_flag = (int *)(tmem_slot + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t mt = (uint32_t)((a.M + 127) / 128), nt = (uint32_t)((a.N + TN - 1) / TN);
+    const uint32_t mt = (uint32_t)((a.M + R::TM - 1) / R::TM), nt = (uint32_t)((a.N + TN - 1) / TN);
     const uint32_t ntiles = a.groups * mt * nt;       // below 2^31
+    // this block's place in its pair, and the pair's (or block's) among all
+    const int rank = PAIR ? (int)tc::cluster_rank() : 0;
+    const uint32_t first = PAIR ? blockIdx.x / 2 : blockIdx.x;
+    const uint32_t stride = PAIR ? gridDim.x / 2 : gridDim.x;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < R::FULLS; i++)
-            tc::mbar_init(&full[i], 1 + 32);          // the TMA loads, each lane's scales
+            // the loads (in the leader both blocks'), each lane's scales, and word
+            // that the other block's scales are there
+            tc::mbar_init(&full[i], 1 + 32 + (PAIR ? 1 : 0));
+        for (int i = 0; i < R::SRING; i++)
+            tc::mbar_init(&scaled[i], 32);
         for (int i = 0; i < R::STAGES; i++)
             tc::mbar_init(&empty[i], 1);
         for (int i = 0; i < R::NBUF; i++) {
             tc::mbar_init(&accf[i], 1);
-            tc::mbar_init(&acce[i], R::EPI);
+            tc::mbar_init(&acce[i], 8);               // epilogue warps of a unit
         }
         tc::mbar_init(done, 2);                       // both issuers
         tc::fence_mbar_init();
@@ -127,11 +147,18 @@ proj_rows_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         tc::tma_prefetch_desc(&tmW);
     }
     if (warp == 1) {
-        tc::tmem_alloc(tmem_slot, 512);
-        tc::tmem_relinquish();
+        if constexpr (PAIR) {
+            tc::tmem_alloc_pair(tmem_slot, 512);
+            tc::tmem_relinquish_pair();
+        } else {
+            tc::tmem_alloc(tmem_slot, 512);
+            tc::tmem_relinquish();
+        }
     }
     tc::fence_before();
     __syncthreads();
+    if constexpr (PAIR)
+        tc::cluster_sync();                           // the other block's barriers stand
     tc::fence_after();
     const uint32_t tmem = *tmem_slot;
     volatile int *abortv = abort_flag;
@@ -144,17 +171,25 @@ proj_rows_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         mi = (int)(r - grp * mt);
     };
 
+    auto commit = [](uint64_t *bar) {
+        if constexpr (PAIR)
+            tc::mma_commit_pair(bar);
+        else
+            tc::mma_commit(bar);
+    };
+
     if (warp < 4) {
-        if constexpr (TN == 256)
-            tc::regs_down<32>();
+        if constexpr (PAIR)
+            tc::regs_down<40>();
         if (warp == 0) {
             // ---------------- operands
             uint32_t it = 0;
             bool ok = true;
-            for (uint32_t t = blockIdx.x; t < ntiles && ok; t += gridDim.x) {
+            for (uint32_t t = first; t < ntiles && ok; t += stride) {
                 int grp, mi, ni;
                 coords(t, grp, mi, ni);
-                const int ax = grp * a.K, ay = mi * 128, wy = grp * a.N + ni * TN;
+                const int ax = grp * a.K, ay = mi * R::TM + rank * 128;
+                const int wy = grp * a.N + ni * TN + rank * R::UROWS;
                 for (int b = 0; b < a.nb; b++, it++) {
                     const int st = it % R::STAGES;
                     if (it >= R::STAGES &&
@@ -164,9 +199,20 @@ proj_rows_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                     }
                     if (tc::elect_one()) {
                         uint64_t *landed = &full[it % R::FULLS];
-                        tc::mbar_arrive_expect_tx(landed, R::A_BYTES + R::B_BYTES);
-                        tc::tma_load_2d(sA + st * R::A_BYTES, &tmA, landed, ax + b * PB, ay);
-                        tc::tma_load_2d(sB + st * R::B_BYTES, &tmW, landed, b * PB, wy);
+                        if constexpr (PAIR) {
+                            if (rank == 0)
+                                tc::mbar_arrive_expect_tx(landed, 2 * (R::A_BYTES + R::B_BYTES));
+                            const uint32_t at = tc::cluster_map(landed, 0);
+                            tc::tma_load_2d_pair(sA + st * R::A_BYTES, &tmA, at, ax + b * PB, ay);
+#pragma unroll
+                            for (int h = 0; h < R::UPB; h++)
+                                tc::tma_load_2d_pair(sB + st * R::B_BYTES + h * R::UROWS * PB, &tmW,
+                                                     at, b * PB, wy + h * 128);
+                        } else {
+                            tc::mbar_arrive_expect_tx(landed, R::A_BYTES + R::B_BYTES);
+                            tc::tma_load_2d(sA + st * R::A_BYTES, &tmA, landed, ax + b * PB, ay);
+                            tc::tma_load_2d(sB + st * R::B_BYTES, &tmW, landed, b * PB, wy);
+                        }
                     }
                     __syncwarp();
                 }
@@ -175,19 +221,26 @@ proj_rows_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                 *abort_flag = 1;
                 report(a.err, CSA_ERR_TIMEOUT, K_FP8_PROJ, blockIdx.x, 0);
             }
-            // let the copies in flight land before the block exits
+            // let the copies in flight land before the block exits (the leader
+            // knows of both blocks')
             volatile int never = 0;
-            for (uint32_t j = it > R::STAGES ? it - R::STAGES : 0; j < it; j++)
-                static_cast<void>(tc::mbar_wait(&full[j % R::FULLS], (j / R::FULLS) & 1, &never,
-                                                200000000ull));
+            for (uint32_t j = it > R::STAGES ? it - R::STAGES : 0; j < it; j++) {
+                if (rank == 0)
+                    static_cast<void>(tc::mbar_wait(&full[j % R::FULLS], (j / R::FULLS) & 1, &never,
+                                                    200000000ull));
+                // and the leader's commits arrive
+                if (PAIR)
+                    static_cast<void>(tc::mbar_wait(&empty[j % R::STAGES], (j / R::STAGES) & 1,
+                                                    &never, 200000000ull));
+            }
         } else if (warp == 3) {
             // ---------------- scales: four tokens' to a lane, and the features'
             uint32_t it = 0;
             bool ok = true;
-            for (uint32_t t = blockIdx.x; t < ntiles && ok; t += gridDim.x) {
+            for (uint32_t t = first; t < ntiles && ok; t += stride) {
                 int grp, mi, ni;
                 coords(t, grp, mi, ni);
-                const int64_t r0 = (int64_t)mi * 128 + lane;
+                const int64_t r0 = (int64_t)mi * R::TM + rank * 128 + lane;
                 const int rows = (int)(a.M - r0 < 128 ? a.M - r0 : 128);   // may be negative
                 const float *as = a.As + (rows > 0 ? r0 * a.las + (int64_t)grp * a.nb : 0);
                 const bool has_w = lane < TN / 128 && ni * TN + lane * 128 < a.N;
@@ -209,7 +262,7 @@ proj_rows_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                                       i * 32 < rows ? 4 : 0);
                     if (lane < TN / 128)
                         tc::cp_async4(slot + 128 + lane, ws + b, has_w ? 4 : 0);
-                    tc::cp_async_arrive(&full[it % R::FULLS]);
+                    tc::cp_async_arrive(rank == 0 ? &full[it % R::FULLS] : &scaled[it % R::SRING]);
                 }
             }
             if (!ok && lane == 0) {
@@ -217,90 +270,143 @@ proj_rows_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                 report(a.err, CSA_ERR_TIMEOUT, K_FP8_PROJ, blockIdx.x, 6);
             }
             tc::cp_async_wait_all();
-        } else {
+        } else if (rank == 0) {
             // ---------------- MMA issuers: the whole warp runs the loop (so that
             // what it computes stays in uniform registers), one lane issues
-            constexpr uint32_t idesc = tc::idesc_e4m3(128, TN);
+            constexpr uint32_t idesc = tc::idesc_e4m3(R::TM, 128);
             const uint64_t dA = tc::sdesc_sw128(tc::smem_u32(sA)), dB = tc::sdesc_sw128(tc::smem_u32(sB));
-            const uint32_t total = (ntiles - blockIdx.x + gridDim.x - 1) / gridDim.x * a.nb;
+            const uint32_t total = (ntiles - first + stride - 1) / stride * a.nb;
             bool ok = true;
             for (uint32_t it = warp - 1; it < total; it += 2) {
-                const uint32_t st = it % R::STAGES, buf = it % R::NBUF;
-                const uint32_t pa = (it / R::NBUF - 1) & 1, pf = (it / R::FULLS) & 1;
+                const uint32_t st = it % R::STAGES, buf0 = it * R::UPB % R::NBUF;
+                const uint32_t pa = (it * R::UPB / R::NBUF - 1) & 1, pf = (it / R::FULLS) & 1;
                 uint64_t *landed = &full[it % R::FULLS];
-                // both barriers tried before either answer is used: one round trip
-                // to shared memory
-                const bool free = it < R::NBUF || tc::mbar_test_wait(&acce[buf], pa);
+                // all barriers tried before any answer is used: one round trip to
+                // shared memory
+                bool free[R::UPB];
+#pragma unroll
+                for (int h = 0; h < R::UPB; h++)
+                    free[h] = it * R::UPB < R::NBUF || tc::mbar_test_wait(&acce[buf0 + h], pa);
                 ok = tc::mbar_test_wait(landed, pf) || tc::mbar_wait_sleep(landed, pf, abortv);
-                ok = ok && (free || tc::mbar_wait_sleep(&acce[buf], pa, abortv));
+#pragma unroll
+                for (int h = 0; h < R::UPB; h++) {
+                    ok = ok && (free[h] || tc::mbar_wait_sleep(&acce[buf0 + h], pa, abortv));
+                    if (!ok)
+                        break;
+                    tc::fence_after();
+                    if (tc::elect_one()) {
+                        const uint32_t d = tmem + (buf0 + h) * 128;
+                        const uint64_t da = dA + ((st * R::A_BYTES) >> 4);
+                        const uint64_t db = dB + ((st * R::B_BYTES + h * R::UROWS * PB) >> 4);
+#pragma unroll
+                        for (int kk = 0; kk < PB / UK; kk++) {
+                            if constexpr (PAIR)
+                                tc::mma_f8_pair(d, da + (kk * UK >> 4), db + (kk * UK >> 4), idesc,
+                                                kk != 0);
+                            else
+                                tc::mma_f8(d, da + (kk * UK >> 4), db + (kk * UK >> 4), idesc,
+                                           kk != 0);
+                        }
+                        if (h == R::UPB - 1)
+                            commit(&empty[st]);
+                        commit(&accf[buf0 + h]);
+                    }
+                    __syncwarp();
+                }
                 if (!ok)
                     break;
-                tc::fence_after();
-                if (tc::elect_one()) {
-                    const uint64_t da = dA + ((st * R::A_BYTES) >> 4);
-                    const uint64_t db = dB + ((st * R::B_BYTES) >> 4);
-#pragma unroll
-                    for (int kk = 0; kk < PB / UK; kk++)
-                        tc::mma_f8(tmem + buf * TN, da + (kk * UK >> 4), db + (kk * UK >> 4), idesc,
-                                   kk != 0);
-                    tc::mma_commit(&empty[st]);
-                    tc::mma_commit(&accf[buf]);
-                }
-                __syncwarp();
             }
             if (!ok && lane == 0) {
                 *abort_flag = 1;
                 report(a.err, CSA_ERR_TIMEOUT, K_FP8_PROJ, blockIdx.x, 1);
             }
             __syncwarp();
-            if (tc::elect_one())
-                tc::mma_commit(done);
+            if (tc::elect_one()) {
+                if constexpr (PAIR)
+                    tc::mma_commit_pair_own(done);
+                else
+                    tc::mma_commit(done);
+            }
             __syncwarp();
             volatile int never = 0;
             static_cast<void>(tc::mbar_wait(done, 0, &never, 200000000ull));
+        } else if (warp == 1) {
+            // ---------------- the second block's word to the leader: a block's MMAs
+            // wait for both blocks' scales, so that they are there when the sums
+            // are, and nobody runs ahead of them
+            const uint32_t total = (ntiles - first + stride - 1) / stride * a.nb;
+            bool ok = true;
+            for (uint32_t it = 0; it < total && ok; it++) {
+                ok = tc::mbar_wait_sleep(&scaled[it % R::SRING], (it / R::SRING) & 1, abortv);
+                if (ok && tc::elect_one())
+                    tc::mbar_arrive_cluster(tc::cluster_map(&full[it % R::FULLS], 0));
+                __syncwarp();
+            }
+            if (!ok && lane == 0) {
+                *abort_flag = 1;
+                report(a.err, CSA_ERR_TIMEOUT, K_FP8_PROJ, blockIdx.x, 7);
+            }
         }
         __syncwarp();
     } else {
-        if constexpr (TN == 256)
-            tc::regs_up<112>();
+        if constexpr (PAIR)
+            tc::regs_up<232>();
         // ---------------- epilogue: lane quarter warp % 4 = 32 tokens, the
-        // features c0 .. c0 + 63 of the tile
-        const int e = warp - 4, q4 = warp & 3, c0 = (e >> 2) * 64;
-        const uint32_t lane_addr = tmem + ((uint32_t)(q4 * 32) << 16) + c0;
+        // features c0 .. c0 + CW - 1 of the tile
+        constexpr int CW = R::CW, BOXES = CW / 64;    // boxes of a warp: 32 tokens x 128 bytes
+        const int e = warp - 4, q4 = warp & 3, c0 = (e >> 2) * CW;
+        const uint32_t lane_addr = tmem + ((uint32_t)(q4 * 32) << 16) + c0 % 128;
+        const uint32_t acce0 = PAIR ? tc::cluster_map(acce, 0) : 0u;   // the leader's
         uint8_t *stage = sO + e * R::OUT_BYTES;
-        const int pair = 1 + (e >> 3) * 4 + q4;       // barrier with the warp of the other 64 of 128
+        // barrier with the warp of the other half of a scale's block (CW = 64)
+        const int other = 1 + (e >> 3) * 4 + q4;
         uint32_t it = 0;
-        for (uint32_t t = blockIdx.x; t < ntiles; t += gridDim.x) {
-            float2 acc[32];
+        bool sums = false;                            // block it seen to be summed
+        auto look = [&] {
+            const uint32_t u = it * R::UPB + c0 / 128;  // this warp's unit of block it
+            sums = tc::mbar_test_wait(&accf[u % R::NBUF], (u / R::NBUF) & 1);
+        };
+        for (uint32_t t = first; t < ntiles; t += stride) {
+            float2 acc[CW / 2];
 #pragma unroll
-            for (int j = 0; j < 32; j++)
+            for (int j = 0; j < CW / 2; j++)
                 acc[j] = make_float2(0.f, 0.f);
             bool ok = true;
-            for (int b = 0; b < a.nb; b++, it++) {
-                const uint32_t buf = it % R::NBUF;
-                ok = tc::mbar_wait_sleep(&accf[buf], (it / R::NBUF) & 1, abortv);
+            look();
+            for (int b = 0; b < a.nb; b++) {
+                const uint32_t u = it * R::UPB + c0 / 128, buf = u % R::NBUF;
+                ok = sums || tc::mbar_wait_sleep(&accf[buf], (u / R::NBUF) & 1, abortv);
                 if (!ok)
                     break;
                 tc::fence_after();
-                // landed before the MMAs of this block were let go
+                uint32_t v[2][32];
+                tc::tmem_ld32(lane_addr + buf * 128, v[0]);
                 const float *slot = sS + it % R::SRING * R::SLOT;
                 const float s = slot[q4 * 32 + lane] * slot[128 + c0 / 128];
                 const float2 s2 = make_float2(s, s);
+                it++;
 #pragma unroll
-                for (int c = 0; c < 2; c++) {
-                    uint32_t v[32];
-                    tc::tmem_get(lane_addr + buf * TN + c * 32, v);
-                    if (c == 1) {
+                for (int c = 0; c < CW / 32; c++) {
+                    tc::tmem_ld_wait(v[c & 1]);
+                    if (c + 1 < CW / 32) {
+                        tc::tmem_ld32(lane_addr + buf * 128 + (c + 1) * 32, v[(c + 1) & 1]);
+                    } else {
                         tc::fence_before();
                         __syncwarp();
-                        if (lane == 0)
-                            tc::mbar_arrive(&acce[buf]);
+                        if (lane == 0) {
+                            if constexpr (PAIR)
+                                tc::mbar_arrive_cluster(acce0 + buf * 8);
+                            else
+                                tc::mbar_arrive(&acce[buf]);
+                        }
+                        look();                       // answered while the last sums are added
                     }
 #pragma unroll
                     for (int j = 0; j < 16; j++)
-                        acc[c * 16 + j] = __ffma2_rn(
-                            make_float2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])), s2,
-                            acc[c * 16 + j]);
+                        acc[c * 16 + j] =
+                            __ffma2_rn(make_float2(__uint_as_float(v[c & 1][2 * j]),
+                                                   __uint_as_float(v[c & 1][2 * j + 1])),
+                                       s2, acc[c * 16 + j]);
                 }
             }
             if (!ok) {
@@ -310,43 +416,63 @@ proj_rows_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             int grp, mi, ni;
             coords(t, grp, mi, ni);
             const int n0 = ni * TN + c0;              // first feature, within the group
-            const int cols = a.N - n0 < 64 ? a.N - n0 : 64;   // may be negative
-            const int col = grp * a.N + n0, y0 = mi * 128 + q4 * 32;
+            const int cols = a.N - n0 < CW ? a.N - n0 : CW;   // may be negative
+            const int col = grp * a.N + n0, y0 = mi * R::TM + rank * 128 + q4 * 32;
+            // in the store's 128-byte swizzle: piece p of row r at p ^ r % 8
+            auto put = [&](uint8_t *box, int piece, uint32_t w0, uint32_t w1, uint32_t w2,
+                           uint32_t w3) {
+                *(uint4 *)(box + lane * 128 + ((piece ^ (lane & 7)) << 4)) =
+                    make_uint4(w0, w1, w2, w3);
+            };
+            auto send = [&](const uint8_t *box, int from) {
+                if (lane == 0 && y0 < a.M && from < cols)
+                    tc::tma_store_2d(&tmO, box, col + from, y0);
+            };
             if (a.out_dt == CSA_E4M3) {
-                // the scale's block is this warp's 64 features and the other's; both
-                // fill the first one's box
-                uint8_t *box = sO + (e & ~4) * R::OUT_BYTES;
                 float m = 0.f;                         // features behind the last are zero
 #pragma unroll
-                for (int j = 0; j < 32; j++)
+                for (int j = 0; j < CW / 2; j++)
                     m = max_mag(m, acc[j]);
-                sM[e * 32 + lane] = m;
-                if ((e & 4) == 0 && lane == 0)
+                uint8_t *box = stage;
+                if (lane == 0)
                     tc::bulk_wait_read();
-                if (tc::named_bar_or(pair, 64, !ok))
-                    break;
-                const float sc = block_scale(max_nan(m, sM[(e ^ 4) * 32 + lane]));
-                if ((e & 4) == 0 && y0 + lane < a.M && cols > 0)
+                if constexpr (CW == 64) {
+                    // a scale's block is two warps': both fill the first one's box
+                    box = sO + (e & ~4) * R::OUT_BYTES;
+                    sM[e * 32 + lane] = m;
+                    if (tc::named_bar_or(other, 64, !ok))
+                        break;
+                    m = max_nan(m, sM[(e ^ 4) * 32 + lane]);
+                } else {
+                    __syncwarp();
+                    if (!ok)
+                        break;
+                }
+                const bool lead = CW == 128 || (e & 4) == 0;
+                const float sc = block_scale(m);
+                if (lead && y0 + lane < a.M && cols > 0)
                     a.out_scale[(int64_t)(y0 + lane) * a.nbo + col / 128] = sc;
-                uint32_t w[16];
-                codes_of<16>(acc, sc, w);
+                uint32_t w[CW / 4];
+                codes_of<CW / 4>(acc, sc, w);
 #pragma unroll
-                for (int j = 0; j < 4; j++)
-                    *(uint4 *)(box + lane * 128 + ((((e & 4) + j) ^ (lane & 7)) << 4)) =
-                        make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+                for (int j = 0; j < CW / 16; j++)
+                    put(box, (lead ? 0 : 4) + j, w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
                 tc::fence_async_shared();
-                tc::named_bar_sync(pair, 64);
-                if ((e & 4) == 0 && lane == 0 && y0 < a.M && cols > 0) {
-                    tc::tma_store_2d(&tmO, box, col, y0);
-                    tc::bulk_commit();
+                if constexpr (CW == 64)
+                    tc::named_bar_sync(other, 64);
+                else
+                    __syncwarp();
+                if (lead) {
+                    send(box, 0);
+                    if (lane == 0)
+                        tc::bulk_commit();
                 }
                 continue;
             }
             if (!ok)
                 break;
             if (a.tma_out) {
-                // boxes of 32 tokens x 128 bytes, in the store's 128-byte swizzle
-                // (piece p of row r at p ^ r % 8): one in bf16, two in float32
+                // 64 features to a box in bf16, 32 in float32, whose warp goes twice
 #pragma unroll
                 for (int h = 0; h < 2; h++) {
                     if (h && a.out_dt == CSA_BF16)
@@ -354,33 +480,35 @@ proj_rows_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                     if (lane == 0)
                         tc::bulk_wait_read();
                     __syncwarp();
+                    if (a.out_dt == CSA_BF16) {
 #pragma unroll
-                    for (int j = 0; j < 8; j++) {
-                        uint4 w;
-                        if (a.out_dt == CSA_BF16)
-                            w = make_uint4(bf16_2(acc[4 * j].x, acc[4 * j].y),
-                                           bf16_2(acc[4 * j + 1].x, acc[4 * j + 1].y),
-                                           bf16_2(acc[4 * j + 2].x, acc[4 * j + 2].y),
-                                           bf16_2(acc[4 * j + 3].x, acc[4 * j + 3].y));
-                        else
-                            w = make_uint4(__float_as_uint(acc[h * 16 + 2 * j].x),
-                                           __float_as_uint(acc[h * 16 + 2 * j].y),
-                                           __float_as_uint(acc[h * 16 + 2 * j + 1].x),
-                                           __float_as_uint(acc[h * 16 + 2 * j + 1].y));
-                        *(uint4 *)(stage + lane * 128 + ((j ^ (lane & 7)) << 4)) = w;
+                        for (int j = 0; j < CW / 8; j++)
+                            put(stage + j / 8 * 4096, j % 8, bf16_2(acc[4 * j].x, acc[4 * j].y),
+                                bf16_2(acc[4 * j + 1].x, acc[4 * j + 1].y),
+                                bf16_2(acc[4 * j + 2].x, acc[4 * j + 2].y),
+                                bf16_2(acc[4 * j + 3].x, acc[4 * j + 3].y));
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < CW / 8; j++) {
+                            const float2 p = acc[h * CW / 4 + 2 * j], q = acc[h * CW / 4 + 2 * j + 1];
+                            put(stage + j / 8 * 4096, j % 8, __float_as_uint(p.x),
+                                __float_as_uint(p.y), __float_as_uint(q.x), __float_as_uint(q.y));
+                        }
                     }
                     tc::fence_async_shared();
                     __syncwarp();
-                    if (lane == 0 && y0 < a.M && h * 32 < cols) {
-                        tc::tma_store_2d(&tmO, stage, col + h * 32, y0);
+                    const int width = a.out_dt == CSA_BF16 ? 64 : 32;
+#pragma unroll
+                    for (int i = 0; i < BOXES; i++)
+                        send(stage + i * 4096, h * CW / 2 + i * width);
+                    if (lane == 0)
                         tc::bulk_commit();
-                    }
                 }
             } else if (y0 + lane < a.M) {
                 // rows that no tensor map describes (not a multiple of 16 bytes)
                 const int64_t o = (int64_t)(y0 + lane) * a.ldo + col;
 #pragma unroll
-                for (int j = 0; j < 64; j++) {
+                for (int j = 0; j < CW; j++) {
                     const float v = j & 1 ? acc[j / 2].y : acc[j / 2].x;
                     if (j < cols) {
                         if (a.out_dt == CSA_BF16)
@@ -396,9 +524,14 @@ proj_rows_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     }
     tc::fence_before();
     __syncthreads();
+    if constexpr (PAIR)
+        tc::cluster_sync();                           // nothing more arrives from the other block
     if (warp == 1) {
         tc::fence_after();
-        tc::tmem_dealloc(tmem, 512);
+        if constexpr (PAIR)
+            tc::tmem_dealloc_pair(tmem, 512);
+        else
+            tc::tmem_dealloc(tmem, 512);
     }
 }
 
@@ -799,15 +932,15 @@ int sm_count()
     return sms;
 }
 
-template <int TN>
+template <bool PAIR>
 cudaError_t launch_rows(const Fp8ProjArgs &g, ProjDev d, int sms, cudaStream_t s)
 {
-    using R = Rows<TN>;
+    using R = Rows<PAIR>;
     CUtensorMap tmA, tmW, tmO;
     if (!make_tmap_2d(&tmA, g.A, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)g.M,
                       (uint64_t)g.groups * g.K, 128) ||
         !make_tmap_2d(&tmW, g.W, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, (uint64_t)d.ldo, (uint64_t)g.K,
-                      TN))
+                      R::UROWS))
         return cudaErrorInvalidValue;
     const int es = g.out_dt == CSA_F32 ? 4 : g.out_dt == CSA_BF16 ? 2 : 1;
     d.tma_out = d.ldo * es % 16 == 0;
@@ -819,16 +952,25 @@ cudaError_t launch_rows(const Fp8ProjArgs &g, ProjDev d, int sms, cudaStream_t s
                                              : CU_TENSOR_MAP_DATA_TYPE_UINT8,
                       es, (uint64_t)g.M, (uint64_t)d.ldo, 32))
         return cudaErrorInvalidValue;
-    cudaError_t e = cudaFuncSetAttribute(proj_rows_kernel<TN>,
+    cudaError_t e = cudaFuncSetAttribute(proj_rows_kernel<PAIR>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, (int)R::SMEM);
     if (e != cudaSuccess)
         return e;
-    const int64_t tiles = (g.M + 127) / 128 * ((g.N + TN - 1) / TN) * g.groups;
+    const int64_t tiles = (g.M + R::TM - 1) / R::TM * ((g.N + R::TN - 1) / R::TN) * g.groups;
     if (tiles > INT32_MAX)
         return cudaErrorInvalidConfiguration;
-    proj_rows_kernel<TN><<<(unsigned)(tiles < sms ? tiles : sms), R::THREADS, R::SMEM, s>>>(
-        tmA, tmW, tmO, d);
-    return cudaGetLastError();
+    const int64_t room = PAIR ? sms / 2 : sms;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((tiles < room ? tiles : room) * (PAIR ? 2 : 1)));
+    cfg.blockDim = dim3(R::THREADS);
+    cfg.dynamicSmemBytes = R::SMEM;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim = {2, 1, 1};
+    cfg.attrs = at;
+    cfg.numAttrs = PAIR ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, proj_rows_kernel<PAIR>, tmA, tmW, tmO, d);
 }
 
 template <int TT>
@@ -919,9 +1061,9 @@ cudaError_t launch_fp8_proj(const Fp8ProjArgs &g, unsigned *err, cudaStream_t s)
     const int64_t cols_tiles = (g.M + 63) / 64 * ((g.N + 127) / 128) * g.groups;
     if (d.nb >= 16 && 2 * cols_tiles <= sms)
         return launch_cols<64>(g, d, sms, s);
-    if (tiles <= 2 * sms)
-        return launch_rows<128>(g, d, sms, s);
-    return launch_rows<256>(g, d, sms, s);
+    if (tiles <= 2 * sms || g.M < 512)
+        return launch_rows<false>(g, d, sms, s);
+    return launch_rows<true>(g, d, sms, s);
 }
 
 }  // namespace csa
