@@ -3,19 +3,23 @@
 //   r[t, j] = sum_b As[t, b] Ws[j / 128, b] sum_{k in block b} A[t, k] W[j, k],
 // blocks b of 128 inputs, float32 sums; bf16, float32 or e4m3 results.
 //
-// Both kernels feed the 5th-generation tensor cores (kind::f8f6f4) from a TMA
-// ring whose stages are one block of 128 inputs: the products of a block are
-// summed in tensor memory from zero, and the epilogue warps add the block's
+// The first two kernels feed the 5th-generation tensor cores (kind::f8f6f4) from
+// a TMA ring whose stages are one block of 128 inputs: the products of a block
+// are summed in tensor memory from zero, and the epilogue warps add the block's
 // sum, times its scale, to float32 registers while the next block's MMAs run
 // into another tensor-memory buffer. (The scales are arbitrary floats, one per
 // token and block, so they cannot ride in the MMA itself.)
 //
 // proj_rows_kernel (many tokens): tokens on the MMA's M axis, so that an
-// epilogue thread owns one token and multiplies a block's sums by one scale.
-// proj_cols_kernel (few tokens): features on the M axis and tokens on N, so
-// that one token costs a 16-wide MMA and not a 128-row one; the blocks of
-// inputs are split over a cluster of thread blocks, whose partial results are
-// added through distributed shared memory in the order of their ranks.
+// epilogue thread owns one token and multiplies a block's sums by one scale;
+// large calls by pairs of thread blocks (cta_group::2).
+// proj_cols_kernel (9 to 32 tokens, and more over long rows): features on the M
+// axis and tokens on N, so that one token costs a 16-wide MMA and not a 128-row
+// one; the blocks of inputs are split over a cluster of thread blocks, whose
+// partial results are added through distributed shared memory in the order of
+// their ranks.
+// proj_few_kernel (up to 8 tokens): warp MMAs straight from global memory.
+// launch_fp8_proj says where one gives way to the next.
 //
 // Every wait is bounded; on expiry the kernel records CSA_ERR_TIMEOUT, lets
 // its copies and products land and returns.
@@ -52,27 +56,37 @@ __device__ __forceinline__ uint32_t bf16_2(float a, float b)
 // ------------------------------------------------------------ many tokens
 
 // Tiles of 128 tokens x 128 features, or (PAIR) of 256 x 256 by two thread
-// blocks whose tensor cores work as one: a block brings 128 tokens and 128 of
+// blocks whose tensor cores work as one: a block brings 128 tokens and half of
 // the features, and holds the sums of its tokens and all features. Warp 0 issues
 // the TMA loads, warps 1 and 2 (of the leader) in turn the MMAs of a block of
-// inputs, warp 3 copies the scales, TN / 16 epilogue warps each own a TMEM lane
-// quarter (32 tokens) and 64 features. Tensor memory holds 512 / TN accumulators
-// of one block each.
-// A pair, because one block's tile of 128 x 256 is bound by shared memory: per
-// block of inputs the loads write 48 KB and the MMAs read 48 KB, 750 cycles at
-// 128 bytes a cycle where the MMAs take 512; in a pair it is 32 and 32 KB.
-// Two issuers, because an issuer goes on only when its last MMA has started,
-// and then needs some 450 cycles for its next barriers and issues, which the
-// other's MMAs hide. Sixteen epilogue warps with 64 sums a thread, because eight
-// with 128 could not overlap their loads from tensor memory (about 300 cycles
-// of its port a block) with their sums (256 cycles of the FMA pipe) and took
-// 1050 cycles a block; they take registers over from the first warpgroup (32 +
-// 4 x 112 = 5 x 96). Scales are copied to shared memory as far ahead as the
-// operands (read by the epilogue itself, or by a warp that loads and then stores
-// them, their latency was the pace: 1000 cycles a block). Results leave through
-// shared memory by TMA stores that run beside the next tile's products (stored
-// from the registers, 32 rows to a store instruction, a tile's results held its
-// epilogue for 6400 cycles, as long as seven blocks of inputs).
+// inputs, warp 3 copies the scales, the epilogue warps each own a TMEM lane
+// quarter (32 tokens) and CW features. A block's MMAs go in units of 128
+// features, of which tensor memory holds four.
+// What the form of a pair's tile answers to (grouped output projection, 16384
+// tokens x 8 groups of 4096 -> 1024, in a graph at 1965 MHz):
+// - One block's tile of 128 x 256 is bound by shared memory: per block of inputs
+//   the loads write 48 KB and the MMAs read 48 KB, 750 cycles at 128 bytes a
+//   cycle where the MMAs take 512. A pair writes 32 KB in each block. 545 us
+//   became 510 us (2.16 PFLOP/s, tensor pipe 62 % busy).
+// - From an accumulator's last MMA to the next one into it pass about 1100
+//   cycles of barriers, besides its draining, which two whole-block buffers do
+//   not cover: units of half a block, with two buffers each, made 302 us of 316
+//   on 32768 x 8192 x 1024 (e4m3 results).
+// - An issuer goes on only when its last MMA has started, and then needs some
+//   450 cycles for its next barriers and issues, which the other's MMAs hide.
+// - Adding the sums is bound by instructions: 128 x 256 float32 FMAs a block are
+//   256 of the FMA pipe's cycles, and every warp pays its barriers and addresses
+//   a block. Eight warps of 128 features, on the registers that the first
+//   warpgroup gives up (40 + 2 x 232 = 3 x 168), take 510 us, sixteen of 64
+//   features 590 us.
+// - Scales are copied to shared memory as far ahead as the operands (read by the
+//   epilogue itself, or by a warp that loads and then stores them, their latency
+//   was the pace: 1000 cycles a block).
+// - Results leave through shared memory by TMA stores that run beside the next
+//   tile's products (stored from the registers, 32 rows to a store instruction, a
+//   tile's results held its epilogue for 6400 cycles).
+// Under load the board's power cap holds the clock near 1.5 GHz: sustained, the
+// same call takes 595 us.
 template <bool PAIR> struct Rows {
     static constexpr int TN = PAIR ? 256 : 128;       // features of a tile
     static constexpr int TM = PAIR ? 256 : 128;       // tokens of a tile
@@ -1041,29 +1055,32 @@ cudaError_t launch_fp8_proj(const Fp8ProjArgs &g, unsigned *err, cudaStream_t s)
     d.out_dt = g.out_dt;
     d.tma_out = false;
     const int sms = sm_count();
-    // 128 x 128 tiles that the call has
-    const int64_t tiles = (g.M + 127) / 128 * ((g.N + 127) / 128) * g.groups;
     // Up to 8 tokens take the kernel that waits least, but for e4m3 results (a
-    // scale's 128 features would have to share a block) and for weights of many
-    // short rows, which the ring streams better (8 tokens by 32768 x 1024: 9.7
-    // against 10.6 us; by 16384 x 4096: 19.1 against 18.4 us).
-    const int64_t few_tiles = (int64_t)g.groups * ((g.N + 15) / 16);
-    if (g.M <= kFewTokens && g.out_dt != CSA_E4M3 && (d.nb >= 16 || few_tiles < 8 * (int64_t)sms))
+    // scale's 128 features would have to share a block) and for large weights,
+    // which the ring streams better (8 tokens by 4096 x 4096: 5.9 against 6.2 us;
+    // by 16384 x 2048: 10.1 against 8.3).
+    if (g.M <= kFewTokens && g.out_dt != CSA_E4M3 && d.ldo * g.K <= (24 << 20))
         return launch_few(g, d, sms, s);
     if (g.M <= 16)
         return launch_cols<16>(g, d, sms, s);
     if (g.M <= 32)
         return launch_cols<32>(g, d, sms, s);
-    // More tokens take the row kernel, unless its tiles would leave half the SMs
-    // idle over long rows, which a cluster shares (333 tokens by 1000 x 2064:
-    // 9.3 against 11.1 us; 128 by 1024 x 4096: 9.2 against 12.1; but 100 by 8192
-    // x 1024: 7.7 against 6.0).
+    // More tokens take the row kernel, unless long rows over few tiles leave a
+    // cluster several SMs to a tile (128 tokens by 1024 x 4096: 11.5 against 9.2
+    // us; 100 by 4096 x 2048: 7.4 against 8.9). Rows whose starts are not 32-byte
+    // aligned cost the row kernel's loads more (333 tokens by 1000 x 2048: 7.5
+    // against 8.9 us; by 1000 x 2064: 10.4 against 9.1).
     const int64_t cols_tiles = (g.M + 63) / 64 * ((g.N + 127) / 128) * g.groups;
-    if (d.nb >= 16 && 2 * cols_tiles <= sms)
+    if (d.nb >= 16 && (g.K % 32 == 0 ? 4 : 2) * cols_tiles <= sms)
         return launch_cols<64>(g, d, sms, s);
-    if (tiles <= 2 * sms || g.M < 512)
-        return launch_rows<false>(g, d, sms, s);
-    return launch_rows<true>(g, d, sms, s);
+    // A pair's tile is four of a single block's and takes 16/9 of its time on two
+    // SMs (4096 tokens by 2048 x 4096: 39.9 us in four rounds against 35.6 in two;
+    // 1536 by 4096 x 4096: 31.0 in three against 35.0 in two).
+    const int64_t one = (g.M + 127) / 128 * ((g.N + 127) / 128) * g.groups;
+    const int64_t two = (g.M + 255) / 256 * ((g.N + 255) / 256) * g.groups;
+    if (16 * ((two + sms / 2 - 1) / (sms / 2)) < 9 * ((one + sms - 1) / sms))
+        return launch_rows<true>(g, d, sms, s);
+    return launch_rows<false>(g, d, sms, s);
 }
 
 }  // namespace csa
