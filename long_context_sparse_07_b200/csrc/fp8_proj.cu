@@ -100,6 +100,7 @@ template <bool PAIR> struct Rows {
     static constexpr int CW = PAIR ? 128 : 64;        // features of an epilogue warp
     static constexpr int EPI = 4 * TN / CW;
     static constexpr int THREADS = 128 + 32 * EPI;
+    static constexpr int REGS_DOWN = 40, REGS_UP = 232;   // of PAIR's warpgroups
     static constexpr uint32_t A_BYTES = 128 * PB, B_BYTES = 128 * PB;   // of each block
     static constexpr int UROWS = 128 / UPB;           // features a block brings to a unit
     static constexpr uint32_t OUT_BYTES = 64 * CW;    // of each epilogue warp: store boxes
@@ -194,7 +195,7 @@ proj_rows_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
 
     if (warp < 4) {
         if constexpr (PAIR)
-            tc::regs_down<40>();
+            tc::regs_down<R::REGS_DOWN>();
         if (warp == 0) {
             // ---------------- operands
             uint32_t it = 0;
@@ -364,7 +365,7 @@ proj_rows_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         __syncwarp();
     } else {
         if constexpr (PAIR)
-            tc::regs_up<232>();
+            tc::regs_up<R::REGS_UP>();
         // ---------------- epilogue: lane quarter warp % 4 = 32 tokens, the
         // features c0 .. c0 + CW - 1 of the tile
         constexpr int CW = R::CW, BOXES = CW / 64;    // boxes of a warp: 32 tokens x 128 bytes
@@ -443,7 +444,14 @@ proj_rows_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                     tc::tma_store_2d(&tmO, box, col + from, y0);
             };
             if (a.out_dt == CSA_E4M3) {
-                float m = 0.f;                         // features behind the last are zero
+                // features behind the last have sums of zero, which an infinite
+                // scale makes NaN
+                if (cols < CW)
+#pragma unroll
+                    for (int j = 0; j < CW / 2; j++)
+                        if (2 * j >= cols)             // N is a multiple of 16
+                            acc[j] = make_float2(0.f, 0.f);
+                float m = 0.f;
 #pragma unroll
                 for (int j = 0; j < CW / 2; j++)
                     m = max_mag(m, acc[j]);
@@ -782,6 +790,10 @@ proj_cols_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         const int cols = a.N - n0 - lane * 4;         // features of this lane that exist
         const int64_t t = t0 + j, o = t * a.ldo + (int64_t)grp * a.N + n0 + lane * 4;
         if (a.out_dt == CSA_E4M3) {
+            // features behind the last have sums of zero, which an infinite scale
+            // makes NaN; N is a multiple of 16
+            if (cols <= 0)
+                v = make_float4(0.f, 0.f, 0.f, 0.f);
             const float2 p[2] = {make_float2(v.x, v.y), make_float2(v.z, v.w)};
             float m = max_mag(max_mag(0.f, p[0]), p[1]);
 #pragma unroll
@@ -792,7 +804,7 @@ proj_cols_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             codes_of<1>(p, s, w);
             if (lane == 0)
                 a.out_scale[t * a.nbo + fb] = s;
-            if (cols > 0)                              // N is a multiple of 16
+            if (cols > 0)
                 *(uint32_t *)((uint8_t *)a.out + o) = w[0];
         } else if (a.ldo % 4 == 0) {
             if (cols > 0) {
@@ -831,8 +843,8 @@ proj_cols_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
 // Up to 8 tokens: the weight's bytes are all that counts, and what a call waits
 // for. A warp takes 16 features and a share of the input blocks: 16-byte loads
 // of the weight straight into the fragments of 16 x 8 x 32 warp MMAs (no tensor
-// memory to allocate, no ring to fill: one token by 1024 x 4096 takes 4.3 us in
-// a graph, against 5.9 us through the kernel above), the loads of four blocks
+// memory to allocate, no ring to fill: one token by 1024 x 4096 takes 4.4 us in
+// a graph, against 4.9 us through the kernel above), the loads of four blocks
 // in flight before the first is used. Which inputs share an MMA does not matter
 // as long as both operands agree: lane (g, t) = (lane / 4, lane % 4) holds
 // inputs 16 t .. 16 t + 15 of every 64, eight for each of two MMAs, of features
@@ -973,6 +985,16 @@ cudaError_t launch_rows(const Fp8ProjArgs &g, ProjDev d, int sms, cudaStream_t s
     const int64_t tiles = (g.M + R::TM - 1) / R::TM * ((g.N + R::TN - 1) / R::TN) * g.groups;
     if (tiles > INT32_MAX)
         return cudaErrorInvalidConfiguration;
+    if (PAIR) {
+        // the warpgroups' shares (regs_down, regs_up) come out of the launch's
+        // registers: with fewer the epilogue would wait for ever
+        static const int regs = [] {
+            cudaFuncAttributes f;
+            return cudaFuncGetAttributes(&f, proj_rows_kernel<PAIR>) == cudaSuccess ? f.numRegs : 0;
+        }();
+        if (regs * R::THREADS < 128 * R::REGS_DOWN + (R::THREADS - 128) * R::REGS_UP)
+            return cudaErrorInvalidConfiguration;
+    }
     const int64_t room = PAIR ? sms / 2 : sms;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((tiles < room ? tiles : room) * (PAIR ? 2 : 1)));

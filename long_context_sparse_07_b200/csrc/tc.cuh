@@ -253,12 +253,6 @@ __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N)
            ((uint32_t)(M >> 4) << 24);
 }
 
-}  // namespace tc
-}  // namespace csa
-
-namespace csa {
-namespace tc {
-
 // 32 / 16 consecutive 32-bit columns written to this thread's TMEM lane.
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32])
 {
@@ -318,12 +312,6 @@ __device__ __forceinline__ void cp_async_wait_all()
     asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-}  // namespace tc
-}  // namespace csa
-
-namespace csa {
-namespace tc {
-
 // Barrier among the `count` threads of named barrier `id` (id 0 is
 // __syncthreads); returns true on every thread if `pred` held on any.
 __device__ __forceinline__ bool named_bar_or(int id, int count, bool pred)
@@ -341,12 +329,6 @@ __device__ __forceinline__ void named_bar_sync(int id, int count)
 {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
 }
-
-}  // namespace tc
-}  // namespace csa
-
-namespace csa {
-namespace tc {
 
 __device__ __forceinline__ void cp_async_commit()
 {
@@ -368,12 +350,6 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8])
                  : "r"(taddr));
 }
 
-}  // namespace tc
-}  // namespace csa
-
-namespace csa {
-namespace tc {
-
 // Adds `bytes` to the transaction count the current phase of `bar` waits
 // for, without arriving.
 __device__ __forceinline__ void mbar_expect_tx(uint64_t *bar, uint32_t bytes)
@@ -381,12 +357,6 @@ __device__ __forceinline__ void mbar_expect_tx(uint64_t *bar, uint32_t bytes)
     asm volatile("mbarrier.expect_tx.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes)
                  : "memory");
 }
-
-}  // namespace tc
-}  // namespace csa
-
-namespace csa {
-namespace tc {
 
 // Waits for this thread's tensor-memory loads and hands the loaded registers
 // on, so that no use of them can be scheduled before the wait.
@@ -399,14 +369,6 @@ __device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[32])
                    "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
                    "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]),
                    "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
-}
-
-__device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[16])
-{
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
-                   "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
-                   "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
 }
 
 // Rank of this block in its cluster; the hardware barrier over all threads of
@@ -447,12 +409,6 @@ __device__ __forceinline__ float4 cluster_ld4(const void *local, uint32_t rank)
     return v;
 }
 
-}  // namespace tc
-}  // namespace csa
-
-namespace csa {
-namespace tc {
-
 // Moves registers between warpgroups: every warp of a warpgroup executes it.
 // The shares after all moves add up to at most the launch's registers.
 template <int N> __device__ __forceinline__ void regs_down()
@@ -463,20 +419,6 @@ template <int N> __device__ __forceinline__ void regs_up()
 {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
-
-// 32 bytes to a 32-byte aligned address: a whole sector.
-__device__ __forceinline__ void st_global_32(void *p, const uint32_t (&w)[8])
-{
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
-                 "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                 : "memory");
-}
-
-}  // namespace tc
-}  // namespace csa
-
-namespace csa {
-namespace tc {
 
 // One try that sleeps in the hardware for up to `ns` nanoseconds.
 __device__ __forceinline__ bool mbar_try_sleep(uint64_t *bar, uint32_t parity, uint32_t ns = 20000)
@@ -513,12 +455,6 @@ __device__ __forceinline__ bool elect_one()
     return ok != 0;
 }
 
-}  // namespace tc
-}  // namespace csa
-
-namespace csa {
-namespace tc {
-
 // Box of shared memory to global memory (coordinates not negative; what lies
 // behind the tensor's end is left out), in this thread's current bulk group.
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, const void *src, int x, int y)
@@ -543,12 +479,6 @@ __device__ __forceinline__ void bulk_wait_all()
 {
     asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
-
-}  // namespace tc
-}  // namespace csa
-
-namespace csa {
-namespace tc {
 
 // 32 or 16 consecutive 32-bit columns of this thread's TMEM lane, waited for:
 // one statement, so that no use of the registers can come before the wait.
@@ -581,12 +511,6 @@ __device__ __forceinline__ void tmem_get(uint32_t taddr, uint32_t (&r)[16])
         : "r"(taddr)
         : "memory");
 }
-
-}  // namespace tc
-}  // namespace csa
-
-namespace csa {
-namespace tc {
 
 // 4-byte asynchronous global -> shared copy; src_bytes = 0 zero-fills.
 __device__ __forceinline__ void cp_async4(void *dst, const void *src, uint32_t src_bytes)

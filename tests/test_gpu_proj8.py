@@ -173,6 +173,19 @@ def test_add_norm_quant_special_values():
     abi.csa_get_error()
 
 
+@pytest.mark.parametrize("rows,d", [(3, 64), (2, 4096), (2, 32768), (400, 20480)])
+def test_add_norm_quant_sum_that_overflows_gives_zeros(rows, d):
+    """Squares of 2^65 are beyond float32, those of 2^50 are not yet."""
+    x = torch.full((rows, d), 2.0 ** 50, device=DEV)
+    x[1] = 2.0 ** 65
+    y, codes = torch.empty_like(x), torch.empty(rows, d, device=DEV, dtype=F8)
+    scale = torch.empty(rows, nb(d), device=DEV)
+    abi.csa_add_norm_quant(x, y=y, codes=codes, scale=scale)
+    assert (y[1] == 0).all() and (codes[1].float() == 0).all() and (scale[1] == 2.0 ** -126).all()
+    # all equal values: the norm is 1, off by the tolerance of the norm
+    assert ((y[0] - 1).abs() <= (d / 64 + 40) * U).all()
+
+
 # ---------------------------------------------------------------- weight
 
 @pytest.mark.parametrize("N,K,dt", [
@@ -292,6 +305,22 @@ def test_fp8_proj_zero_rows_blocks_and_special_codes(M, N, K):
         c, s = run(ops, N, F8, 1)
         assert c.float()[0].isnan().all() and s[0].isnan().all()
         assert (c.float()[1] == 0).all() and (s[1] == 2.0 ** -126).all()
+
+
+@pytest.mark.parametrize("M,N,K", [(5, 272, 256), (30, 144, 2048), (60, 272, 2048),
+                                   (200, 272, 128), (2500, 4112, 272)])
+def test_fp8_proj_infinite_rows_behind_the_last_feature(M, N, K):
+    """The last scale block holds 16 features: the tile's others, which are not
+    there, leave the scale of a row with an infinite scale infinite (not NaN) and
+    its finite neighbours alone."""
+    A, As, W, Ws = operands(17 + M, M, N, K)
+    A[3], W[:], As[3, 0] = 0x38, 0x38, np.inf     # ones: every sum of row 3 is positive
+    c, s = run(device(A, As, W, Ws), N, F8, 1)
+    assert torch.isinf(s[3]).all() and not c.float()[4].isnan().any()
+    fine = [r for r in range(M) if r != 3]
+    assert torch.isfinite(s[fine]).all()
+    f32, _ = run(device(A, As, W, Ws), N, torch.float32, 1)
+    assert torch.isposinf(f32[3]).all() and torch.isfinite(f32[fine]).all()
 
 
 def test_fp8_proj_rows_do_not_depend_on_the_batch():
