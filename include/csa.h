@@ -371,7 +371,9 @@ csa_status csa_grouped_out_proj(const void *o, const void *Wg, const void *Wo, i
  *   v = s / sqrt(mean_j s_j^2 + eps) * gamma   (v = s when !normalise)
  *   total <- s, y <- v, (codes, scale) <- v
  * all in float32 until the one rounding of each output (the norm reads s
- * before it is rounded to total).
+ * before it is rounded to total). The sum of squares is a float32 too: a row
+ * whose sum overflows (no earlier than at magnitudes of 2^55) is normed to
+ * zeros.
  * Arguments:
  *   x         [rows, d] of dt (F32 or BF16).
  *   residual  [rows, d] of dt, or NULL.
@@ -397,8 +399,8 @@ csa_status csa_add_norm_quant(const void *x, const void *residual, const float *
  * csa_quantize_weight -- a weight in the form csa_fp8_proj reads: W [N, K] of
  * dt (F32 or BF16) to codes [N, K] e4m3 and scale [ceil(N / 128),
  * ceil(K / 128)] float32. A NaN reaches its whole block.
- * Requirements: N >= 0 (0 is a no-op); K a multiple of 16, K >= 16; W and
- *   codes 16-byte aligned; no overlap.
+ * Requirements: 0 <= N <= 2^30 (0 is a no-op); K a multiple of 16,
+ *   16 <= K <= 2^30; W and codes 16-byte aligned; no overlap.
  */
 csa_status csa_quantize_weight(const void *W, csa_dtype dt, int64_t N, int K, void *codes,
                                float *scale, void *stream);
@@ -423,7 +425,7 @@ csa_status csa_quantize_weight(const void *W, csa_dtype dt, int64_t N, int K, vo
  * gives the same bits; M may choose another order of the sums.
  * Requirements: 0 <= M <= INT32_MAX (0 is a no-op); N >= 1; K a multiple of
  *   16, K >= 16; groups >= 1, and N and K multiples of 128 when groups > 1;
- *   N a multiple of 16 for E4M3; groups N and groups K at most INT32_MAX; A, W
+ *   N a multiple of 16 for E4M3; groups N and groups K at most 2^30; A, W
  *   and out 16-byte aligned; out and out_scale overlap no other operand.
  */
 csa_status csa_fp8_proj(const void *A, const float *A_scale, const void *W, const float *W_scale,

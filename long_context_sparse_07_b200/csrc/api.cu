@@ -44,6 +44,9 @@ bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
 bool aligned4(const void *p) { return ((uintptr_t)p & 3u) == 0; }
 bool pow2(int64_t x) { return x > 0 && (x & (x - 1)) == 0; }
 
+// Of a projection: so that an index rounded up to a tile stays an int.
+constexpr int64_t kMaxFeatures = 1 << 30;
+
 csa_status launched(cudaError_t e, const char *what)
 {
     if (e != cudaSuccess)
@@ -477,7 +480,8 @@ csa_status csa_quantize_weight(const void *W, csa_dtype dt, int64_t N, int K, vo
     const char *w = "csa_quantize_weight";
     REQUIRE(dt == CSA_F32 || dt == CSA_BF16, CSA_ERR_UNSUPPORTED, "%s: dtype must be F32 or BF16",
             w);
-    REQUIRE(N >= 0 && N <= INT32_MAX, CSA_ERR_INVALID_ARG, "%s: bad N", w);
+    REQUIRE(N >= 0 && N <= kMaxFeatures && K <= kMaxFeatures, CSA_ERR_INVALID_ARG, "%s: bad N / K",
+            w);
     REQUIRE(K >= 16 && K % 16 == 0, CSA_ERR_UNSUPPORTED, "%s: K = %d must be a multiple of 16", w,
             K);
     if (N == 0)
@@ -501,7 +505,7 @@ csa_status csa_fp8_proj(const void *A, const float *A_scale, const void *W, cons
             "%s: bad M / N / groups", w);
     REQUIRE(K >= 16 && K % 16 == 0, CSA_ERR_UNSUPPORTED, "%s: K = %d must be a multiple of 16", w,
             K);
-    REQUIRE((int64_t)groups * N <= INT32_MAX && (int64_t)groups * K <= INT32_MAX,
+    REQUIRE((int64_t)groups * N <= kMaxFeatures && (int64_t)groups * K <= kMaxFeatures,
             CSA_ERR_INVALID_ARG, "%s: groups N or groups K too large", w);
     REQUIRE(groups == 1 || (N % 128 == 0 && K % 128 == 0), CSA_ERR_UNSUPPORTED,
             "%s: several groups need N and K multiples of 128", w);

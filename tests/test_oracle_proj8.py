@@ -117,6 +117,7 @@ def test_quantize_weight_refuses(lib):
     assert call(W=P + 8) == -1 and call(codes=2 * P + 1) == -1 and call(scale=3 * P + 2) == -1
     assert call(codes=P) == -1
     assert call(N=0, W=None, codes=None, scale=None) == 0
+    assert call(N=2 ** 30 + 1) == -1 and call(K=2 ** 30 + 16) == -1
 
 
 def test_fp8_proj_refuses(lib):
@@ -140,6 +141,8 @@ def test_fp8_proj_refuses(lib):
         assert call(**{k: 9 * P + 2}) == -1 and b"aligned" in lib.csa_last_message(), k
     assert call(out=P) == -1 and b"overlap" in lib.csa_last_message()
     assert call(M=0, A=None, As=None, W=None, Ws=None, out=None) == 0
+    assert call(N=2 ** 30 + 1) == -1 and call(K=2 ** 30 + 16) == -1
+    assert call(groups=2, N=2 ** 30) == -1
 
 
 def test_bindings_refuse_host_tensors_and_wrong_shapes():
