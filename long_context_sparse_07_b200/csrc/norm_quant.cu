@@ -29,14 +29,43 @@ constexpr int kThreads = 256;
 constexpr int kLane = 16;         // consecutive values of a lane
 constexpr int kPairs = kLane / 2;
 
-// 16 consecutive values as they lie in memory.
+// 16 consecutive values as they lie in memory, moved as sectors of 32 bytes
+// where the buffers' alignment allows (WIDE), else in halves.
 template <typename T> struct Raw {
     uint4 u[sizeof(T)];
-    __device__ __forceinline__ void load(const T *p)
+    __device__ __forceinline__ void load(const T *p, bool wide)
     {
+        const uint4 *q = (const uint4 *)p;
+        if (wide) {
 #pragma unroll
-        for (int i = 0; i < (int)sizeof(T); i++)
-            u[i] = ((const uint4 *)p)[i];
+            for (int i = 0; i < (int)sizeof(T); i += 2)
+                asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                             : "=r"(u[i].x), "=r"(u[i].y), "=r"(u[i].z), "=r"(u[i].w),
+                               "=r"(u[i + 1].x), "=r"(u[i + 1].y), "=r"(u[i + 1].z),
+                               "=r"(u[i + 1].w)
+                             : "l"(q + i)
+                             : "memory");
+        } else {
+#pragma unroll
+            for (int i = 0; i < (int)sizeof(T); i++)
+                u[i] = q[i];
+        }
+    }
+    __device__ __forceinline__ void store(T *p, bool wide) const
+    {
+        uint4 *q = (uint4 *)p;
+        if (wide) {
+#pragma unroll
+            for (int i = 0; i < (int)sizeof(T); i += 2)
+                asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(q + i),
+                             "r"(u[i].x), "r"(u[i].y), "r"(u[i].z), "r"(u[i].w), "r"(u[i + 1].x),
+                             "r"(u[i + 1].y), "r"(u[i + 1].z), "r"(u[i + 1].w)
+                             : "memory");
+        } else {
+#pragma unroll
+            for (int i = 0; i < (int)sizeof(T); i++)
+                q[i] = u[i];
+        }
     }
     __device__ __forceinline__ float2 pair(int i) const
     {
@@ -47,8 +76,9 @@ template <typename T> struct Raw {
     }
 };
 
-__device__ __forceinline__ void store_16(__nv_bfloat16 *p, const float2 (&v)[kPairs])
+__device__ __forceinline__ void store_16(__nv_bfloat16 *p, const float2 (&v)[kPairs], bool wide)
 {
+    Raw<__nv_bfloat16> r;
 #pragma unroll
     for (int i = 0; i < 2; i++) {
         uint32_t w[4];
@@ -57,14 +87,18 @@ __device__ __forceinline__ void store_16(__nv_bfloat16 *p, const float2 (&v)[kPa
             const __nv_bfloat162 h = __float22bfloat162_rn(v[4 * i + e]);
             w[e] = *(const uint32_t *)&h;
         }
-        ((uint4 *)p)[i] = make_uint4(w[0], w[1], w[2], w[3]);
+        r.u[i] = make_uint4(w[0], w[1], w[2], w[3]);
     }
+    r.store(p, wide);
 }
-__device__ __forceinline__ void store_16(float *p, const float2 (&v)[kPairs])
+__device__ __forceinline__ void store_16(float *p, const float2 (&v)[kPairs], bool wide)
 {
+    Raw<float> r;
 #pragma unroll
     for (int i = 0; i < 4; i++)
-        ((float4 *)p)[i] = make_float4(v[2 * i].x, v[2 * i].y, v[2 * i + 1].x, v[2 * i + 1].y);
+        r.u[i] = make_uint4(__float_as_uint(v[2 * i].x), __float_as_uint(v[2 * i].y),
+                            __float_as_uint(v[2 * i + 1].x), __float_as_uint(v[2 * i + 1].y));
+    r.store(p, wide);
 }
 
 // Largest magnitude of a scale's block: 16 values of each of 8 lanes.
@@ -132,10 +166,10 @@ __device__ __forceinline__ float row_sum(float ss, int tpr, int sub, float *part
 template <typename T>
 __device__ __forceinline__ void write_piece(const float2 (&v)[kPairs], bool live, int64_t base,
                                             int j, int64_t row, int nb, T *y, uint8_t *codes,
-                                            float *scale)
+                                            float *scale, bool wide)
 {
     if (live && y)
-        store_16(y + base + j, v);
+        store_16(y + base + j, v, wide);
     if (codes) {
         const float m = eight_lane_max(block_max(v));
         if (live) {
@@ -151,18 +185,27 @@ __device__ __forceinline__ void write_piece(const float2 (&v)[kPairs], bool live
 // a time; the grid is resident and strides over the rows. A thread's 16 values
 // stay in its registers from the one read to the outputs, so that each byte
 // crosses HBM once and only the sum of squares is exchanged, and its 16 gains
-// for all its rows (read per row they cost more L1 traffic than the row). In
-// bf16 the next row is read while this one is written.
+// for all its rows (read per row they cost more L1 traffic than the row). The
+// next row is read while this one is written: x before the sums are exchanged,
+// the residual after them (both before: 340 against 294 us for 65536 x 4096
+// bf16, with reads and writes crowding each other; with this order a call
+// without a residual, RES = false, takes 213 us, where a test of the pointer in
+// the loop cost 267).
 // A few longer rows are each cut over a cluster of thread blocks (CLUSTER; `cut`
 // values a block), which add their sums of squares in the order of their ranks:
 // one row of 32768 takes 4.7 us in a graph, read twice by one block 9.2 us.
-template <typename T, bool CLUSTER, int MOST>
-__global__ void __launch_bounds__(MOST, sizeof(T) == 2 && MOST == 512 ? 2 : 1)
+constexpr int min_blocks(int size, int most, bool res)
+{
+    // as many registers as the loop takes without spilling much
+    return size == 2 ? (most == 512 ? 2 : 1) : most == 256 ? (res ? 2 : 3) : 1;
+}
+
+template <typename T, bool CLUSTER, int MOST, bool RES>
+__global__ void __launch_bounds__(MOST, min_blocks(sizeof(T), MOST, RES))
 add_norm_quant_kernel(const T *x, const T *residual, const float *__restrict__ gamma,
                       bool gamma_aligned, int64_t rows, int d, int tpr, int cut, int ranks,
-                      float eps, T *total, T *y, uint8_t *codes, float *scale)
+                      float eps, T *total, T *y, uint8_t *codes, float *scale, bool wide)
 {
-    constexpr bool kAhead = sizeof(T) == 2;
     __shared__ float part[2][32];
     __shared__ float sums[2];
     const int rank = CLUSTER ? (int)tc::cluster_rank() : 0;
@@ -180,34 +223,33 @@ add_norm_quant_kernel(const T *x, const T *residual, const float *__restrict__ g
     Raw<T> a, b;
     const int64_t stride = (int64_t)gridDim.x / ranks * rpb, mine = threadIdx.x / tpr;
     int64_t r0 = (int64_t)(blockIdx.x / ranks) * rpb;  // the block's first row
-    auto read = [&](int64_t row) {
-        if (row < rows && in) {
-            a.load(x + row * d + j);
-            if (residual)
-                b.load(residual + row * d + j);
-        }
+    auto read_x = [&](int64_t row) {
+        if (row < rows && in)
+            a.load(x + row * d + j, wide);
     };
-    if (kAhead)
-        read(r0 + mine);
+    auto read_residual = [&](int64_t row) {
+        if (RES && row < rows && in)
+            b.load(residual + row * d + j, wide);
+    };
+    read_x(r0 + mine);
+    read_residual(r0 + mine);
     for (int parity = 0; r0 < rows; r0 += stride, parity ^= 1) {
         const int64_t row = r0 + mine, base = row * d;
         const bool live = row < rows && in;
-        if (!kAhead)
-            read(row);
         float2 v[kPairs];
         float2 ss2 = make_float2(0.f, 0.f);
 #pragma unroll
         for (int e = 0; e < kPairs; e++) {
             v[e] = make_float2(0.f, 0.f);
             if (live)
-                v[e] = residual ? __fadd2_rn(a.pair(e), b.pair(e)) : a.pair(e);
+                v[e] = RES ? __fadd2_rn(a.pair(e), b.pair(e)) : a.pair(e);
             ss2 = __ffma2_rn(v[e], v[e], ss2);
         }
-        if (kAhead)
-            read(row + stride);
-        if (live && total)
-            store_16(total + base + j, v);
+        read_x(row + stride);
+        if (RES && live && total)
+            store_16(total + base + j, v, wide);
         float ss = row_sum(ss2.x + ss2.y, tpr, sub, part[parity]);
+        read_residual(row + stride);
         if (CLUSTER) {
             // the place of one row is written again two rows later, when every
             // block has passed the next row's barrier and so read this one
@@ -223,7 +265,7 @@ add_norm_quant_kernel(const T *x, const T *residual, const float *__restrict__ g
 #pragma unroll
         for (int e = 0; e < kPairs; e++)
             v[e] = __fmul2_rn(__fmul2_rn(v[e], make_float2(inv, inv)), g[e]);
-        write_piece(v, live, base, j, row, nb, y, codes, scale);
+        write_piece(v, live, base, j, row, nb, y, codes, scale, wide);
     }
     if (CLUSTER) {
         // no block leaves while another may still read its sums
@@ -241,7 +283,7 @@ template <typename T>
 __global__ void __launch_bounds__(kLongThreads, sizeof(T) == 2 ? 2 : 1)
 add_norm_quant_long_kernel(const T *x, const T *residual, const float *__restrict__ gamma,
                            bool gamma_aligned, int d, float eps, T *total, T *y, uint8_t *codes,
-                           float *scale)
+                           float *scale, bool wide)
 {
     constexpr int kStep = kLongThreads * kLane;
     __shared__ float part[32];
@@ -251,9 +293,9 @@ add_norm_quant_long_kernel(const T *x, const T *residual, const float *__restric
     Raw<T> a, b;
     auto read = [&](int j) {
         if (j < d) {
-            a.load(x + base + j);
+            a.load(x + base + j, wide);
             if (residual)
-                b.load(residual + base + j);
+                b.load(residual + base + j, wide);
         }
     };
     // the piece read last, and the next one on its way
@@ -280,7 +322,7 @@ add_norm_quant_long_kernel(const T *x, const T *residual, const float *__restric
     for (int j = first; j - first < d; j += kStep) {
         take(j);
         if (j < d && total)
-            store_16(total + base + j, v);
+            store_16(total + base + j, v, wide);
 #pragma unroll
         for (int e = 0; e < kPairs; e++)
             v[e] = __fmul2_rn(v[e], make_float2(inv, inv));
@@ -291,7 +333,7 @@ add_norm_quant_long_kernel(const T *x, const T *residual, const float *__restric
             for (int e = 0; e < kPairs; e++)
                 v[e] = __fmul2_rn(v[e], g[e]);
         }
-        write_piece(v, j < d, base, j, row, nb, y, codes, scale);
+        write_piece(v, j < d, base, j, row, nb, y, codes, scale, wide);
     }
 }
 
@@ -301,7 +343,7 @@ add_norm_quant_long_kernel(const T *x, const T *residual, const float *__restric
 template <typename T, int CH, bool FLAT>
 __global__ void __launch_bounds__(kThreads)
 add_quant_kernel(const T *x, const T *residual, int64_t rows, int d, T *total, T *y,
-                 uint8_t *codes, float *scale)
+                 uint8_t *codes, float *scale, bool wide)
 {
     const int nb = (d + kBlock - 1) / kBlock;
     const int64_t blocks = rows * nb;
@@ -328,9 +370,9 @@ add_quant_kernel(const T *x, const T *residual, int64_t rows, int d, T *total, T
 #pragma unroll
         for (int i = 0; i < CH; i++) {
             if (at[i] >= 0) {
-                a[i].load(x + at[i]);
+                a[i].load(x + at[i], wide);
                 if (residual)
-                    b[i].load(residual + at[i]);
+                    b[i].load(residual + at[i], wide);
             }
         }
 #pragma unroll
@@ -346,9 +388,9 @@ add_quant_kernel(const T *x, const T *residual, int64_t rows, int d, T *total, T
     for (int i = 0; i < CH; i++) {
         if (at[i] >= 0) {
             if (total)
-                store_16(total + at[i], v[i]);
+                store_16(total + at[i], v[i], wide);
             if (y)
-                store_16(y + at[i], v[i]);
+                store_16(y + at[i], v[i], wide);
         }
         if (codes) {
             const float m = eight_lane_max(block_max(v[i]));
@@ -372,7 +414,7 @@ constexpr int kRowStep = kThreads / 8;
 template <typename T>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2)
 quantize_weight_kernel(const T *__restrict__ W, int64_t N, int K, uint8_t *__restrict__ codes,
-                       float *__restrict__ scale)
+                       float *__restrict__ scale, bool wide)
 {
     __shared__ float part[kThreads / 32];
     const int kb = blockIdx.x;
@@ -382,7 +424,7 @@ quantize_weight_kernel(const T *__restrict__ W, int64_t N, int K, uint8_t *__res
 #pragma unroll
     for (int i = 0; i < kPieces; i++) {
         if (n0 + i * kRowStep < N && col < K)
-            a[i].load(W + (n0 + i * kRowStep) * K + col);
+            a[i].load(W + (n0 + i * kRowStep) * K + col, wide);
         else
             a[i] = Raw<T>{};
     }
@@ -416,6 +458,13 @@ quantize_weight_kernel(const T *__restrict__ W, int64_t N, int K, uint8_t *__res
         scale[(int64_t)blockIdx.y * gridDim.x + kb] = s;
 }
 
+// Rows are whole sectors of 32 bytes (16 values), so only the bases count.
+bool sectors(const void *p, const void *q = nullptr, const void *r = nullptr,
+             const void *s = nullptr)
+{
+    return (((uintptr_t)p | (uintptr_t)q | (uintptr_t)r | (uintptr_t)s) & 31u) == 0;
+}
+
 template <typename T, bool FLAT>
 cudaError_t launch_quant(const AddNormQuantArgs &a, cudaStream_t s)
 {
@@ -426,19 +475,19 @@ cudaError_t launch_quant(const AddNormQuantArgs &a, cudaStream_t s)
         return cudaErrorInvalidConfiguration;
     add_quant_kernel<T, CH, FLAT><<<(unsigned)grid, kThreads, 0, s>>>(
         (const T *)a.x, (const T *)a.residual, a.rows, a.d, (T *)a.total, (T *)a.y, a.codes,
-        a.scale);
+        a.scale, sectors(a.x, a.residual, a.total, a.y));
     return cudaGetLastError();
 }
 
-template <typename T, bool CLUSTER, int MOST>
-cudaError_t launch_norm(const AddNormQuantArgs &a, int tpr, int rpb, int cut, int ranks,
+template <typename T, bool CLUSTER, int MOST, bool RES>
+cudaError_t launch_norm_rows(const AddNormQuantArgs &a, int tpr, int rpb, int cut, int ranks,
                         cudaStream_t s)
 {
     int dev = 0, sms = 148, per_sm = 1;
     cudaGetDevice(&dev);
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(
-        &per_sm, add_norm_quant_kernel<T, CLUSTER, MOST>, tpr * rpb, 0);
+        &per_sm, add_norm_quant_kernel<T, CLUSTER, MOST, RES>, tpr * rpb, 0);
     if (e != cudaSuccess)
         return e;
     const int64_t want = (a.rows + rpb - 1) / rpb, room = (int64_t)sms * per_sm / ranks;
@@ -451,10 +500,18 @@ cudaError_t launch_norm(const AddNormQuantArgs &a, int tpr, int rpb, int cut, in
     at[0].val.clusterDim = {(unsigned)ranks, 1, 1};
     cfg.attrs = at;
     cfg.numAttrs = CLUSTER ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, add_norm_quant_kernel<T, CLUSTER, MOST>, (const T *)a.x,
+    return cudaLaunchKernelEx(&cfg, add_norm_quant_kernel<T, CLUSTER, MOST, RES>, (const T *)a.x,
                               (const T *)a.residual, a.gamma, ((uintptr_t)a.gamma & 15u) == 0,
                               a.rows, a.d, tpr, cut, ranks, a.eps, (T *)a.total, (T *)a.y,
-                              a.codes, a.scale);
+                              a.codes, a.scale, sectors(a.x, a.residual, a.total, a.y));
+}
+
+template <typename T, bool CLUSTER, int MOST>
+cudaError_t launch_norm(const AddNormQuantArgs &a, int tpr, int rpb, int cut, int ranks,
+                        cudaStream_t s)
+{
+    return a.residual ? launch_norm_rows<T, CLUSTER, MOST, true>(a, tpr, rpb, cut, ranks, s)
+                      : launch_norm_rows<T, CLUSTER, MOST, false>(a, tpr, rpb, cut, ranks, s);
 }
 
 template <typename T>
@@ -465,6 +522,9 @@ cudaError_t launch_add_norm_quant_t(const AddNormQuantArgs &a, cudaStream_t s)
     const int pieces = a.d / kLane;
     if (pieces <= 512) {
         const int tpr = pieces <= 8 ? 8 : pieces <= 16 ? 16 : (pieces + 31) / 32 * 32;
+        if constexpr (sizeof(T) == 4)
+            if (tpr <= 256)
+                return launch_norm<T, false, 256>(a, tpr, 256 / tpr, a.d, 1, s);
         return launch_norm<T, false, 512>(a, tpr, tpr <= 256 ? 256 / tpr : 1, a.d, 1, s);
     }
     // whole scale blocks to each thread block of the cluster, 4096 values at a
@@ -482,7 +542,8 @@ cudaError_t launch_add_norm_quant_t(const AddNormQuantArgs &a, cudaStream_t s)
                 return launch_norm<T, false, 1024>(a, (pieces + 31) / 32 * 32, 1, a.d, 1, s);
         add_norm_quant_long_kernel<T><<<(unsigned)a.rows, kLongThreads, 0, s>>>(
             (const T *)a.x, (const T *)a.residual, a.gamma, ((uintptr_t)a.gamma & 15u) == 0, a.d,
-            a.eps, (T *)a.total, (T *)a.y, a.codes, a.scale);
+            a.eps, (T *)a.total, (T *)a.y, a.codes, a.scale,
+            sectors(a.x, a.residual, a.total, a.y));
         return cudaGetLastError();
     }
     const int blocks = (nb + ranks - 1) / ranks;
@@ -511,11 +572,11 @@ cudaError_t launch_quantize_weight(const QuantWeightArgs &a, cudaStream_t s)
         if (a.dt == CSA_BF16)
             quantize_weight_kernel<__nv_bfloat16><<<grid, kThreads, 0, s>>>(
                 (const __nv_bfloat16 *)a.W + row0 * a.K, rows, a.K, a.codes + row0 * a.K,
-                a.scale + b0 * nbk);
+                a.scale + b0 * nbk, sectors(a.W));
         else
             quantize_weight_kernel<float><<<grid, kThreads, 0, s>>>(
                 (const float *)a.W + row0 * a.K, rows, a.K, a.codes + row0 * a.K,
-                a.scale + b0 * nbk);
+                a.scale + b0 * nbk, sectors(a.W));
     }
     return cudaGetLastError();
 }
