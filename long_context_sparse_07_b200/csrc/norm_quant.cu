@@ -10,11 +10,13 @@
 // 3 bytes a value (unnormed bf16) an SM has about 16 issue slots for each.
 // Hence packed pairs of float32 (one instruction for two values), quotients
 // without a division, and 16 consecutive values to a lane, so that a scale's
-// block is 8 lanes and its maximum three shuffles for every 16 values. Measured
-// in a graph: 65536 x 4096 bf16 with residual and total 312 us (6.05 TB/s, 0.94
-// of the copy rate; 500 us with a division a value and each row read twice), the
-// unnormed 4096 x 32768 69 us (5.9 TB/s), a weight of 32768 x 1024 19.5 us (5.2
-// TB/s), 8 rows of 4096 3.1 us (the launch).
+// block is 8 lanes and its maximum three shuffles for every 16 values. A lane's
+// values are whole sectors of 32 bytes, moved by one instruction each where the
+// buffers are aligned so (in halves, 16384 x 4096 float32 takes 158 us in place
+// of 130). Measured in a graph: 65536 x 4096 bf16 with residual and total 293 us
+// (6.4 TB/s, the copy rate; 500 us with a division a value and each row read
+// twice), the unnormed 4096 x 32768 69 us (5.9 TB/s), a weight of 32768 x 1024
+// 18.2 us (5.5 TB/s), 8 rows of 4096 3 us (the launch).
 #include "common.cuh"
 #include "kernels.h"
 #include "quant8.cuh"
@@ -30,7 +32,7 @@ constexpr int kLane = 16;         // consecutive values of a lane
 constexpr int kPairs = kLane / 2;
 
 // 16 consecutive values as they lie in memory, moved as sectors of 32 bytes
-// where the buffers' alignment allows (WIDE), else in halves.
+// where the buffers' alignment allows (`wide`), else in halves.
 template <typename T> struct Raw {
     uint4 u[sizeof(T)];
     __device__ __forceinline__ void load(const T *p, bool wide)
@@ -188,12 +190,12 @@ __device__ __forceinline__ void write_piece(const float2 (&v)[kPairs], bool live
 // for all its rows (read per row they cost more L1 traffic than the row). The
 // next row is read while this one is written: x before the sums are exchanged,
 // the residual after them (both before: 340 against 294 us for 65536 x 4096
-// bf16, with reads and writes crowding each other; with this order a call
-// without a residual, RES = false, takes 213 us, where a test of the pointer in
-// the loop cost 267).
+// bf16, with reads and writes crowding each other; a
+// call without a residual, RES = false, takes 201 us, with a test of the pointer
+// in the loop 267).
 // A few longer rows are each cut over a cluster of thread blocks (CLUSTER; `cut`
 // values a block), which add their sums of squares in the order of their ranks:
-// one row of 32768 takes 4.7 us in a graph, read twice by one block 9.2 us.
+// one row of 32768 takes 4.2 us in a graph, read twice by one block 7.6 us.
 constexpr int min_blocks(int size, int most, bool res)
 {
     // as many registers as the loop takes without spilling much
@@ -261,7 +263,7 @@ add_norm_quant_kernel(const T *x, const T *residual, const float *__restrict__ g
             for (int q = 0; q < ranks; q++)
                 ss += tc::cluster_ld(&sums[parity], q);
         }
-        const float inv = 1.f / sqrtf(ss / d + eps);
+        const float inv = rsqrtf(ss / d + eps);
 #pragma unroll
         for (int e = 0; e < kPairs; e++)
             v[e] = __fmul2_rn(__fmul2_rn(v[e], make_float2(inv, inv)), g[e]);
@@ -276,10 +278,10 @@ add_norm_quant_kernel(const T *x, const T *residual, const float *__restrict__ g
 
 // Many rows too long for a block's registers, one to a block, are read a second
 // time (from L2) for the outputs; the cluster's barrier a row would cost more
-// (4096 rows of 32768: 339 against 214 us).
+// (4096 rows of 32768: 343 against 195 us).
 constexpr int kLongThreads = 512;
 
-template <typename T>
+template <typename T, bool RES>
 __global__ void __launch_bounds__(kLongThreads, sizeof(T) == 2 ? 2 : 1)
 add_norm_quant_long_kernel(const T *x, const T *residual, const float *__restrict__ gamma,
                            bool gamma_aligned, int d, float eps, T *total, T *y, uint8_t *codes,
@@ -294,7 +296,7 @@ add_norm_quant_long_kernel(const T *x, const T *residual, const float *__restric
     auto read = [&](int j) {
         if (j < d) {
             a.load(x + base + j, wide);
-            if (residual)
+            if (RES)
                 b.load(residual + base + j, wide);
         }
     };
@@ -305,7 +307,7 @@ add_norm_quant_long_kernel(const T *x, const T *residual, const float *__restric
         for (int e = 0; e < kPairs; e++) {
             v[e] = make_float2(0.f, 0.f);
             if (j < d)
-                v[e] = residual ? __fadd2_rn(a.pair(e), b.pair(e)) : a.pair(e);
+                v[e] = RES ? __fadd2_rn(a.pair(e), b.pair(e)) : a.pair(e);
         }
         read(j + kStep);
     };
@@ -318,10 +320,10 @@ add_norm_quant_long_kernel(const T *x, const T *residual, const float *__restric
     }
     read(first);
     const float ss = row_sum(ss2.x + ss2.y, kLongThreads, threadIdx.x, part);
-    const float inv = 1.f / sqrtf(ss / d + eps);
+    const float inv = rsqrtf(ss / d + eps);
     for (int j = first; j - first < d; j += kStep) {
         take(j);
-        if (j < d && total)
+        if (RES && j < d && total)
             store_16(total + base + j, v, wide);
 #pragma unroll
         for (int e = 0; e < kPairs; e++)
@@ -536,11 +538,15 @@ cudaError_t launch_add_norm_quant_t(const AddNormQuantArgs &a, cudaStream_t s)
     int dev = 0, sms = 148;
     cudaGetDevice(&dev);
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (a.rows * ranks > sms) {
-        if constexpr (sizeof(T) == 2)                 // float32 would spill
+    if (a.rows * ranks > sms) {                       // no longer at once by clusters
+        // resident rows up to 16384 (4096 of them: 85 us, read twice 107); in
+        // float32 they would spill
+        if constexpr (sizeof(T) == 2)
             if (pieces <= 1024)
                 return launch_norm<T, false, 1024>(a, (pieces + 31) / 32 * 32, 1, a.d, 1, s);
-        add_norm_quant_long_kernel<T><<<(unsigned)a.rows, kLongThreads, 0, s>>>(
+        const auto kernel =
+            a.residual ? add_norm_quant_long_kernel<T, true> : add_norm_quant_long_kernel<T, false>;
+        kernel<<<(unsigned)a.rows, kLongThreads, 0, s>>>(
             (const T *)a.x, (const T *)a.residual, a.gamma, ((uintptr_t)a.gamma & 15u) == 0, a.d,
             a.eps, (T *)a.total, (T *)a.y, a.codes, a.scale,
             sectors(a.x, a.residual, a.total, a.y));
