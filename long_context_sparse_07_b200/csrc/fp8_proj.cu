@@ -21,6 +21,12 @@
 // proj_few_kernel (up to 8 tokens): warp MMAs straight from global memory.
 // launch_fp8_proj says where one gives way to the next.
 //
+// All are launched so that they may start while the call before them ends (the
+// projections of a step follow one another); the two for few tokens bring their
+// weights into L2 meanwhile. In a graph the norm and projections of one token
+// (13 launches) take 36.6 us so, 47.0 without the weights' prefetch and 51.2
+// with plain launches; of 32 tokens 52, 53.5 and 70 us.
+//
 // Every wait is bounded; on expiry the kernel records CSA_ERR_TIMEOUT, lets
 // its copies and products land and returns.
 #include "common.cuh"
@@ -175,6 +181,8 @@ proj_rows_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     if constexpr (PAIR)
         tc::cluster_sync();                           // the other block's barriers stand
     tc::fence_after();
+    tc::grid_let_next();
+    tc::grid_wait();
     const uint32_t tmem = *tmem_slot;
     volatile int *abortv = abort_flag;
     // tile t -> (group, m tile, n tile), n fastest: the blocks working at one
@@ -629,6 +637,12 @@ proj_cols_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
+    tc::grid_let_next();
+    // the weight does not wait for the call before this one
+    if (warp == 0 && tc::elect_one())
+        for (int b = b0; b < b1; b++)
+            tc::prefetch_l2_2d(&tmW, b * PB, grp * a.N + n0);
+    tc::grid_wait();
     const uint32_t tmem = *tmem_slot;
     volatile int *abortv = abort_flag;
 
@@ -857,9 +871,10 @@ constexpr int kFewLd = kFewTokens + 1;                // padded against bank con
 __device__ __forceinline__ uint4 ld_stream(const uint8_t *p)
 {
     uint4 v;
-    asm("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-        : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-        : "l"(p));
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p)
+                 : "memory");
     return v;
 }
 
@@ -873,10 +888,11 @@ __device__ __forceinline__ void mma_16x8x32(float (&d)[4], uint32_t a0, uint32_t
 }
 
 __global__ void __launch_bounds__(32 * kFewWarps)
-proj_few_kernel(const uint8_t *__restrict__ A, const uint8_t *__restrict__ W, const ProjDev a,
+proj_few_kernel(const uint8_t *A, const uint8_t *W, const ProjDev a,
                 const int ks)
 {
     extern __shared__ float sums[];                   // [ks][16 rg][kFewLd]
+    tc::grid_let_next();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int rg = blockDim.x / 32 / ks, share = warp / rg, group = warp % rg;
     const int rows = 16 * rg;                         // features of the block
@@ -891,6 +907,13 @@ proj_few_kernel(const uint8_t *__restrict__ A, const uint8_t *__restrict__ W, co
     const uint8_t *x0 = A + ((int64_t)(tok ? g : 0) * a.groups + grp) * a.K;
     const float *as = a.As + (int64_t)grp * a.nb;
     const float *ws = a.Ws + ((int64_t)grp * a.N + (f0 < a.N ? f0 : 0)) / PB * a.nb;
+    // the weight does not wait for the call before this one
+    for (int k = b0 * PB + (lane & 7) * PB; k < b1 * PB && k < a.K; k += 8 * PB)
+#pragma unroll
+        for (int r = lane >> 3; r < 16; r += 4)
+            if (f0 + r < a.N)
+                tc::prefetch_l2(W + ((int64_t)grp * a.N + f0 + r) * a.K + k);
+    tc::grid_wait();
     const uint4 zero = make_uint4(0, 0, 0, 0);
     float acc[4] = {0.f, 0.f, 0.f, 0.f};              // (feature g + 8 (e / 2), token 2 t + e % 2)
     for (int b = b0; b < b1; b += kFewAhead) {
@@ -919,7 +942,7 @@ proj_few_kernel(const uint8_t *__restrict__ A, const uint8_t *__restrict__ W, co
 #pragma unroll
             for (int h = 0; h < 2; h++) {
                 const int k = (b + i) * PB + h * 64 + t * 16;
-                const uint4 x = tok && k < a.K ? __ldg((const uint4 *)(x0 + k)) : zero;
+                const uint4 x = tok && k < a.K ? *(const uint4 *)(x0 + k) : zero;
                 mma_16x8x32(p, wa[i][h].x, wb[i][h].x, wa[i][h].y, wb[i][h].y, x.x, x.y);
                 mma_16x8x32(p, wa[i][h].z, wb[i][h].z, wa[i][h].w, wb[i][h].w, x.z, x.w);
             }
@@ -996,17 +1019,9 @@ cudaError_t launch_rows(const Fp8ProjArgs &g, ProjDev d, int sms, cudaStream_t s
             return cudaErrorInvalidConfiguration;
     }
     const int64_t room = PAIR ? sms / 2 : sms;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((tiles < room ? tiles : room) * (PAIR ? 2 : 1)));
-    cfg.blockDim = dim3(R::THREADS);
-    cfg.dynamicSmemBytes = R::SMEM;
-    cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim = {2, 1, 1};
-    cfg.attrs = at;
-    cfg.numAttrs = PAIR ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, proj_rows_kernel<PAIR>, tmA, tmW, tmO, d);
+    return launch_early(proj_rows_kernel<PAIR>,
+                        dim3((unsigned)((tiles < room ? tiles : room) * (PAIR ? 2 : 1))), R::THREADS,
+                        R::SMEM, PAIR ? 2 : 1, s, tmA, tmW, tmO, d);
 }
 
 template <int TT>
@@ -1029,17 +1044,8 @@ cudaError_t launch_cols(const Fp8ProjArgs &g, ProjDev d, int sms, cudaStream_t s
     int split = 1;
     while (split < kMaxSplit && tiles * split * 2 <= sms && split * 2 <= d.nb)
         split *= 2;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(tiles * split));
-    cfg.blockDim = dim3(C::THREADS);
-    cfg.dynamicSmemBytes = C::SMEM;
-    cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim = {(unsigned)split, 1, 1};
-    cfg.attrs = at;
-    cfg.numAttrs = split > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, proj_cols_kernel<TT>, tmA, tmW, d, split);
+    return launch_early(proj_cols_kernel<TT>, dim3((unsigned)(tiles * split)), C::THREADS, C::SMEM,
+                        split, s, tmA, tmW, d, split);
 }
 
 cudaError_t launch_few(const Fp8ProjArgs &g, const ProjDev &d, int sms, cudaStream_t s)
@@ -1051,9 +1057,8 @@ cudaError_t launch_few(const Fp8ProjArgs &g, const ProjDev &d, int sms, cudaStre
         ks *= 2;
     const int rg = ks >= 8 ? 1 : 8 / ks;
     const int64_t blocks = (int64_t)g.groups * ((g.N + 16 * rg - 1) / (16 * rg));
-    proj_few_kernel<<<(unsigned)blocks, 32 * rg * ks, ks * 16 * rg * kFewLd * 4, s>>>(g.A, g.W, d,
-                                                                                      ks);
-    return cudaGetLastError();
+    return launch_early(proj_few_kernel, dim3((unsigned)blocks), 32 * rg * ks,
+                        ks * 16 * rg * kFewLd * 4, 1, s, g.A, g.W, d, ks);
 }
 
 }  // namespace

@@ -162,6 +162,28 @@ struct GemmArgs {
 };
 cudaError_t launch_gemm_nt(const GemmArgs &g, unsigned *err, cudaStream_t s);
 
+// Launches a kernel that calls tc::grid_wait before it touches global memory:
+// it may start while the kernel before it in the stream ends. `cluster` blocks
+// form a cluster.
+template <typename... P, typename... A>
+cudaError_t launch_early(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem,
+                         unsigned cluster, cudaStream_t s, A... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim = {cluster, 1, 1};
+    cfg.attrs = at;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
 // The 8-bit projections: s = x + residual, its RMSNorm and e4m3 storage
 // (csa_add_norm_quant); a weight's e4m3 storage in 128 x 128 blocks
 // (csa_quantize_weight); the block-scaled product (csa_fp8_proj).

@@ -134,14 +134,14 @@ __device__ __forceinline__ void load_gains(const float *gamma, int j, bool align
     if (aligned) {
 #pragma unroll
         for (int e = 0; e < kPairs; e += 2) {
-            const float4 f = __ldg((const float4 *)(gamma + j + 2 * e));
+            const float4 f = *(const float4 *)(gamma + j + 2 * e);
             g[e] = make_float2(f.x, f.y);
             g[e + 1] = make_float2(f.z, f.w);
         }
     } else {
 #pragma unroll
         for (int e = 0; e < kPairs; e++)
-            g[e] = make_float2(__ldg(gamma + j + 2 * e), __ldg(gamma + j + 2 * e + 1));
+            g[e] = make_float2(gamma[j + 2 * e], gamma[j + 2 * e + 1]);
     }
 }
 
@@ -204,7 +204,7 @@ constexpr int min_blocks(int size, int most, bool res)
 
 template <typename T, bool CLUSTER, int MOST, bool RES>
 __global__ void __launch_bounds__(MOST, min_blocks(sizeof(T), MOST, RES))
-add_norm_quant_kernel(const T *x, const T *residual, const float *__restrict__ gamma,
+add_norm_quant_kernel(const T *x, const T *residual, const float *gamma,
                       bool gamma_aligned, int64_t rows, int d, int tpr, int cut, int ranks,
                       float eps, T *total, T *y, uint8_t *codes, float *scale, bool wide)
 {
@@ -220,6 +220,8 @@ add_norm_quant_kernel(const T *x, const T *residual, const float *__restrict__ g
 #pragma unroll
     for (int e = 0; e < kPairs; e++)
         g[e] = make_float2(1.f, 1.f);
+    tc::grid_let_next();
+    tc::grid_wait();
     if (gamma && in)
         load_gains(gamma, j, gamma_aligned, g);
     Raw<T> a, b;
@@ -283,7 +285,7 @@ constexpr int kLongThreads = 512;
 
 template <typename T, bool RES>
 __global__ void __launch_bounds__(kLongThreads, sizeof(T) == 2 ? 2 : 1)
-add_norm_quant_long_kernel(const T *x, const T *residual, const float *__restrict__ gamma,
+add_norm_quant_long_kernel(const T *x, const T *residual, const float *gamma,
                            bool gamma_aligned, int d, float eps, T *total, T *y, uint8_t *codes,
                            float *scale, bool wide)
 {
@@ -311,6 +313,8 @@ add_norm_quant_long_kernel(const T *x, const T *residual, const float *__restric
         }
         read(j + kStep);
     };
+    tc::grid_let_next();
+    tc::grid_wait();
     read(first);
     for (int j = first; j - first < d; j += kStep) {
         take(j);
@@ -366,6 +370,8 @@ add_quant_kernel(const T *x, const T *residual, int64_t rows, int d, T *total, T
             at[i] = g < blocks && j < d ? (row0 + up) * d + j : -1;
         }
     }
+    tc::grid_let_next();
+    tc::grid_wait();
     float2 v[CH][kPairs];
     {
         Raw<T> a[CH], b[CH];
@@ -415,13 +421,14 @@ constexpr int kRowStep = kThreads / 8;
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2)
-quantize_weight_kernel(const T *__restrict__ W, int64_t N, int K, uint8_t *__restrict__ codes,
-                       float *__restrict__ scale, bool wide)
+quantize_weight_kernel(const T *W, int64_t N, int K, uint8_t *codes, float *scale, bool wide)
 {
     __shared__ float part[kThreads / 32];
     const int kb = blockIdx.x;
     const int64_t n0 = (int64_t)blockIdx.y * kBlock + (threadIdx.x >> 3);
     const int col = kb * kBlock + (threadIdx.x & 7) * kLane;
+    tc::grid_let_next();
+    tc::grid_wait();
     Raw<T> a[kPieces];
 #pragma unroll
     for (int i = 0; i < kPieces; i++) {
@@ -475,10 +482,9 @@ cudaError_t launch_quant(const AddNormQuantArgs &a, cudaStream_t s)
     const int64_t grid = (blocks + kThreads / 8 * CH - 1) / (kThreads / 8 * CH);
     if (grid > INT32_MAX)
         return cudaErrorInvalidConfiguration;
-    add_quant_kernel<T, CH, FLAT><<<(unsigned)grid, kThreads, 0, s>>>(
-        (const T *)a.x, (const T *)a.residual, a.rows, a.d, (T *)a.total, (T *)a.y, a.codes,
-        a.scale, sectors(a.x, a.residual, a.total, a.y));
-    return cudaGetLastError();
+    return launch_early(add_quant_kernel<T, CH, FLAT>, dim3((unsigned)grid), kThreads, 0, 1, s,
+                        (const T *)a.x, (const T *)a.residual, a.rows, a.d, (T *)a.total, (T *)a.y,
+                        a.codes, a.scale, sectors(a.x, a.residual, a.total, a.y));
 }
 
 template <typename T, bool CLUSTER, int MOST, bool RES>
@@ -493,19 +499,12 @@ cudaError_t launch_norm_rows(const AddNormQuantArgs &a, int tpr, int rpb, int cu
     if (e != cudaSuccess)
         return e;
     const int64_t want = (a.rows + rpb - 1) / rpb, room = (int64_t)sms * per_sm / ranks;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((want < room ? want : room) * ranks));
-    cfg.blockDim = dim3(tpr * rpb);
-    cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim = {(unsigned)ranks, 1, 1};
-    cfg.attrs = at;
-    cfg.numAttrs = CLUSTER ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, add_norm_quant_kernel<T, CLUSTER, MOST, RES>, (const T *)a.x,
-                              (const T *)a.residual, a.gamma, ((uintptr_t)a.gamma & 15u) == 0,
-                              a.rows, a.d, tpr, cut, ranks, a.eps, (T *)a.total, (T *)a.y,
-                              a.codes, a.scale, sectors(a.x, a.residual, a.total, a.y));
+    return launch_early(add_norm_quant_kernel<T, CLUSTER, MOST, RES>,
+                        dim3((unsigned)((want < room ? want : room) * ranks)), tpr * rpb, 0, ranks, s,
+                        (const T *)a.x, (const T *)a.residual, a.gamma,
+                        ((uintptr_t)a.gamma & 15u) == 0, a.rows, a.d, tpr, cut, ranks, a.eps,
+                        (T *)a.total, (T *)a.y, a.codes, a.scale,
+                        sectors(a.x, a.residual, a.total, a.y));
 }
 
 template <typename T, bool CLUSTER, int MOST>
@@ -546,11 +545,10 @@ cudaError_t launch_add_norm_quant_t(const AddNormQuantArgs &a, cudaStream_t s)
                 return launch_norm<T, false, 1024>(a, (pieces + 31) / 32 * 32, 1, a.d, 1, s);
         const auto kernel =
             a.residual ? add_norm_quant_long_kernel<T, true> : add_norm_quant_long_kernel<T, false>;
-        kernel<<<(unsigned)a.rows, kLongThreads, 0, s>>>(
-            (const T *)a.x, (const T *)a.residual, a.gamma, ((uintptr_t)a.gamma & 15u) == 0, a.d,
-            a.eps, (T *)a.total, (T *)a.y, a.codes, a.scale,
-            sectors(a.x, a.residual, a.total, a.y));
-        return cudaGetLastError();
+        return launch_early(kernel, dim3((unsigned)a.rows), kLongThreads, 0, 1, s, (const T *)a.x,
+                            (const T *)a.residual, a.gamma, ((uintptr_t)a.gamma & 15u) == 0, a.d,
+                            a.eps, (T *)a.total, (T *)a.y, a.codes, a.scale,
+                            sectors(a.x, a.residual, a.total, a.y));
     }
     const int blocks = (nb + ranks - 1) / ranks;
     return launch_norm<T, true, 512>(a, (blocks * (kBlock / kLane) + 31) / 32 * 32, 1, blocks * kBlock,
@@ -575,16 +573,19 @@ cudaError_t launch_quantize_weight(const QuantWeightArgs &a, cudaStream_t s)
         const int64_t nb = nbn - b0 < kMaxY ? nbn - b0 : kMaxY;
         const int64_t row0 = b0 * kBlock, rows = a.N - row0;
         const dim3 grid(nbk, (unsigned)nb);
+        cudaError_t e;
         if (a.dt == CSA_BF16)
-            quantize_weight_kernel<__nv_bfloat16><<<grid, kThreads, 0, s>>>(
-                (const __nv_bfloat16 *)a.W + row0 * a.K, rows, a.K, a.codes + row0 * a.K,
-                a.scale + b0 * nbk, sectors(a.W));
+            e = launch_early(quantize_weight_kernel<__nv_bfloat16>, grid, kThreads, 0, 1, s,
+                             (const __nv_bfloat16 *)a.W + row0 * a.K, rows, a.K,
+                             a.codes + row0 * a.K, a.scale + b0 * nbk, sectors(a.W));
         else
-            quantize_weight_kernel<float><<<grid, kThreads, 0, s>>>(
-                (const float *)a.W + row0 * a.K, rows, a.K, a.codes + row0 * a.K,
-                a.scale + b0 * nbk, sectors(a.W));
+            e = launch_early(quantize_weight_kernel<float>, grid, kThreads, 0, 1, s,
+                             (const float *)a.W + row0 * a.K, rows, a.K, a.codes + row0 * a.K,
+                             a.scale + b0 * nbk, sectors(a.W));
+        if (e != cudaSuccess)
+            return e;
     }
-    return cudaGetLastError();
+    return cudaSuccess;
 }
 
 }  // namespace csa

@@ -409,6 +409,31 @@ __device__ __forceinline__ float4 cluster_ld4(const void *local, uint32_t rank)
     return v;
 }
 
+// Programmatic launches (launch_early below): the next kernel of the stream may
+// be started once every block of this one has called grid_let_next; it does
+// what needs no global memory and then waits in grid_wait (every thread that
+// touches global memory calls it) until the kernels before it are complete and
+// their writes visible. Its loads are plain ones: what it reads may have been
+// written after it began, which the read-only path does not allow for.
+__device__ __forceinline__ void grid_let_next()
+{
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void grid_wait()
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// Brings a tiled box of global memory into L2. This and prefetch_l2 may run
+// before grid_wait: what is read afterwards comes from L2, where every write
+// lands.
+__device__ __forceinline__ void prefetch_l2_2d(const CUtensorMap *map, int x, int y)
+{
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global [%0, {%1, %2}];" ::"l"((uint64_t)map),
+                 "r"(x), "r"(y)
+                 : "memory");
+}
+
 // Moves registers between warpgroups: every warp of a warpgroup executes it.
 // The shares after all moves add up to at most the launch's registers.
 template <int N> __device__ __forceinline__ void regs_down()

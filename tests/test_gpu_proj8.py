@@ -401,6 +401,80 @@ def test_streams_and_graph_replay():
     abi.csa_get_error()
 
 
+@pytest.mark.parametrize("n", [1, 8, 24, 300, 3000])
+def test_calls_in_a_row_wait_for_each_other(n):
+    """Each call reads what the one before it wrote and overwrites what the one
+    before that read, weights among them; launched one behind the other, in a
+    stream or a graph, they give the bits they give with a wait between them."""
+    d, rounds = 1024, 12
+    gen = torch.Generator().manual_seed(n)
+    Ws = [(torch.randn(d, d, generator=gen) / d ** 0.5).to(DEV, torch.bfloat16) for _ in range(2)]
+    x0 = torch.randn(n, d, generator=gen).to(DEV, torch.bfloat16)
+    x, y = torch.empty_like(x0), torch.empty_like(x0)
+    w8, ws = torch.empty(d, d, device=DEV, dtype=F8), torch.empty(8, 8, device=DEV)
+    h8, hs = torch.empty(n, d, device=DEV, dtype=F8), torch.empty(n, 8, device=DEV)
+    u8s = torch.empty(n, d, device=DEV, dtype=F8), torch.empty(n, 8, device=DEV)
+    log = torch.empty(rounds, n, d, device=DEV, dtype=torch.bfloat16)
+
+    def chain(wait):
+        x.copy_(x0)
+        wait()
+        for r in range(rounds):
+            for call in (lambda: abi.csa_quantize_weight(Ws[r % 2], w8, ws),
+                         lambda: abi.csa_add_norm_quant(x, codes=h8, scale=hs),
+                         lambda: abi.csa_fp8_proj(h8, hs, w8, ws, *u8s),
+                         lambda: abi.csa_fp8_proj(*u8s, w8, ws, y),
+                         lambda: abi.csa_add_norm_quant(y, residual=x, total=x, y=log[r])):
+                call()
+                wait()
+
+    chain(torch.cuda.synchronize)
+    want = log.clone()
+    assert torch.isfinite(want.float()).all() and want.float().abs().max() > 1
+    for _ in range(3):
+        log.zero_()
+        chain(lambda: None)
+        assert torch.equal(log, want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        chain(lambda: None)
+    for _ in range(3):
+        log.zero_()
+        graph.replay()
+        assert torch.equal(log, want)
+    abi.csa_get_error()
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+def test_buffers_that_start_inside_a_sector(dt):
+    """16-byte aligned buffers give the bits of 32-byte aligned ones."""
+    def shifted(t, by=16):
+        raw = torch.zeros(t.numel() * t.element_size() + 64, device=DEV, dtype=torch.uint8)
+        at = by + -raw.data_ptr() % 32
+        out = raw[at:at + t.numel() * t.element_size()].view(t.dtype).view(t.shape)
+        assert out.data_ptr() % 32 == by % 32
+        return out.copy_(t)
+
+    for rows, d in ((5, 144), (9, 4096), (300, 10256), (3, 20480)):
+        x, r = (rows_of(i, rows, d, dt).to(DEV) for i in (1, 2))
+        g = torch.rand(d + 1, device=DEV)[1:]
+        got = []
+        for by in (0, 16):
+            for norm in (True, False):
+                t, y = shifted(torch.zeros_like(x), by), shifted(torch.zeros_like(x), by)
+                c = torch.empty(rows, d, device=DEV, dtype=F8)
+                s = torch.empty(rows, nb(d), device=DEV)
+                abi.csa_add_norm_quant(shifted(x, by), shifted(r, by), g if norm else None, norm,
+                                       total=t, y=y, codes=c, scale=s)
+                got.append([v.clone() for v in (t, y, c.view(torch.uint8), s)])
+            c, s = torch.empty(rows, d, device=DEV, dtype=F8), torch.empty(nb(rows), nb(d), device=DEV)
+            abi.csa_quantize_weight(shifted(x, by), c, s)
+            got.append([c.view(torch.uint8), s])
+        for one, two in zip(got[:3], got[3:]):
+            assert all(torch.equal(p, q) for p, q in zip(one, two))
+    abi.csa_get_error()
+
+
 def test_offsets_past_32_bits():
     """More than 2^32 bytes and 2^31 values of input: the last rows are right."""
     rows, d = 70000, 32768
