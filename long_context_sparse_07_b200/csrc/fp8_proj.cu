@@ -501,51 +501,63 @@ proj_rows_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             }
             if (!ok)
                 break;
-            if (a.tma_out) {
-                // 64 features to a box in bf16, 32 in float32, whose warp goes twice
+            // 64 features to a box in bf16, 32 in float32, whose warp goes twice
 #pragma unroll
-                for (int h = 0; h < 2; h++) {
-                    if (h && a.out_dt == CSA_BF16)
-                        break;
-                    if (lane == 0)
-                        tc::bulk_wait_read();
-                    __syncwarp();
-                    if (a.out_dt == CSA_BF16) {
+            for (int h = 0; h < 2; h++) {
+                const bool half = a.out_dt == CSA_BF16;
+                if (h && half)
+                    break;
+                if (lane == 0)
+                    tc::bulk_wait_read();
+                __syncwarp();
+                if (half) {
 #pragma unroll
-                        for (int j = 0; j < CW / 8; j++)
-                            put(stage + j / 8 * 4096, j % 8, bf16_2(acc[4 * j].x, acc[4 * j].y),
-                                bf16_2(acc[4 * j + 1].x, acc[4 * j + 1].y),
-                                bf16_2(acc[4 * j + 2].x, acc[4 * j + 2].y),
-                                bf16_2(acc[4 * j + 3].x, acc[4 * j + 3].y));
-                    } else {
+                    for (int j = 0; j < CW / 8; j++)
+                        put(stage + j / 8 * 4096, j % 8, bf16_2(acc[4 * j].x, acc[4 * j].y),
+                            bf16_2(acc[4 * j + 1].x, acc[4 * j + 1].y),
+                            bf16_2(acc[4 * j + 2].x, acc[4 * j + 2].y),
+                            bf16_2(acc[4 * j + 3].x, acc[4 * j + 3].y));
+                } else {
 #pragma unroll
-                        for (int j = 0; j < CW / 8; j++) {
-                            const float2 p = acc[h * CW / 4 + 2 * j], q = acc[h * CW / 4 + 2 * j + 1];
-                            put(stage + j / 8 * 4096, j % 8, __float_as_uint(p.x),
-                                __float_as_uint(p.y), __float_as_uint(q.x), __float_as_uint(q.y));
-                        }
+                    for (int j = 0; j < CW / 8; j++) {
+                        const float2 p = acc[h * CW / 4 + 2 * j], q = acc[h * CW / 4 + 2 * j + 1];
+                        put(stage + j / 8 * 4096, j % 8, __float_as_uint(p.x), __float_as_uint(p.y),
+                            __float_as_uint(q.x), __float_as_uint(q.y));
                     }
+                }
+                if (a.tma_out) {
                     tc::fence_async_shared();
                     __syncwarp();
-                    const int width = a.out_dt == CSA_BF16 ? 64 : 32;
 #pragma unroll
                     for (int i = 0; i < BOXES; i++)
-                        send(stage + i * 4096, h * CW / 2 + i * width);
+                        send(stage + i * 4096, h * CW / 2 + i * (half ? 64 : 32));
                     if (lane == 0)
                         tc::bulk_commit();
-                }
-            } else if (y0 + lane < a.M) {
-                // rows that no tensor map describes (not a multiple of 16 bytes)
-                const int64_t o = (int64_t)(y0 + lane) * a.ldo + col;
+                } else {
+                    // rows that no tensor map describes (not a multiple of 16 bytes):
+                    // 32 lanes store a box's row
+                    __syncwarp();
+#pragma unroll 1
+                    for (int r = 0; r < 32 && y0 + r < a.M; r++) {
 #pragma unroll
-                for (int j = 0; j < CW; j++) {
-                    const float v = j & 1 ? acc[j / 2].y : acc[j / 2].x;
-                    if (j < cols) {
-                        if (a.out_dt == CSA_BF16)
-                            ((__nv_bfloat16 *)a.out)[o + j] = __float2bfloat16_rn(v);
-                        else
-                            ((float *)a.out)[o + j] = v;
+                        for (int i = 0; i < BOXES; i++) {
+                            const uint32_t w = *(const uint32_t *)(stage + i * 4096 + r * 128 +
+                                                                   ((lane >> 2 ^ (r & 7)) << 4) +
+                                                                   (lane & 3) * 4);
+                            const int f = half ? i * 64 + 2 * lane : h * CW / 2 + i * 32 + lane;
+                            const int64_t o = (int64_t)(y0 + r) * a.ldo + col + f;
+                            if (!half) {
+                                if (f < cols)
+                                    ((uint32_t *)a.out)[o] = w;
+                            } else {
+                                if (f < cols)
+                                    ((uint16_t *)a.out)[o] = (uint16_t)w;
+                                if (f + 1 < cols)
+                                    ((uint16_t *)a.out)[o + 1] = (uint16_t)(w >> 16);
+                            }
+                        }
                     }
+                    __syncwarp();
                 }
             }
         }
@@ -857,8 +869,8 @@ proj_cols_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
 // Up to 8 tokens: the weight's bytes are all that counts, and what a call waits
 // for. A warp takes 16 features and a share of the input blocks: 16-byte loads
 // of the weight straight into the fragments of 16 x 8 x 32 warp MMAs (no tensor
-// memory to allocate, no ring to fill: one token by 1024 x 4096 takes 4.4 us in
-// a graph, against 4.9 us through the kernel above), the loads of four blocks
+// memory to allocate, no ring to fill: one token by 1024 x 4096 takes 3.3 us in
+// a graph, against 4.0 us through the kernel above), the loads of four blocks
 // in flight before the first is used. Which inputs share an MMA does not matter
 // as long as both operands agree: lane (g, t) = (lane / 4, lane % 4) holds
 // inputs 16 t .. 16 t + 15 of every 64, eight for each of two MMAs, of features
@@ -1083,27 +1095,28 @@ cudaError_t launch_fp8_proj(const Fp8ProjArgs &g, unsigned *err, cudaStream_t s)
     d.tma_out = false;
     const int sms = sm_count();
     // Up to 8 tokens take the kernel that waits least, but for e4m3 results (a
-    // scale's 128 features would have to share a block) and for large weights,
-    // which the ring streams better (8 tokens by 4096 x 4096: 5.9 against 6.2 us;
-    // by 16384 x 2048: 10.1 against 8.3).
-    if (g.M <= kFewTokens && g.out_dt != CSA_E4M3 && d.ldo * g.K <= (24 << 20))
+    // scale's 128 features would have to share a block) and where the ring's
+    // kernel fills the SMs without clusters (8 tokens by 8192 x 8192: 16.6 against
+    // 19.8 us; by 20000 x 4096: 33.5 against 21.0).
+    const int64_t ft = ((g.N + 127) / 128) * (int64_t)g.groups;
+    if (g.M <= kFewTokens && g.out_dt != CSA_E4M3 && 2 * ft <= sms)
         return launch_few(g, d, sms, s);
     if (g.M <= 16)
         return launch_cols<16>(g, d, sms, s);
     if (g.M <= 32)
         return launch_cols<32>(g, d, sms, s);
     // More tokens take the row kernel, unless long rows over few tiles leave a
-    // cluster several SMs to a tile (128 tokens by 1024 x 4096: 11.5 against 9.2
-    // us; 100 by 4096 x 2048: 7.4 against 8.9). Rows whose starts are not 32-byte
-    // aligned cost the row kernel's loads more (333 tokens by 1000 x 2048: 7.5
-    // against 8.9 us; by 1000 x 2064: 10.4 against 9.1).
-    const int64_t cols_tiles = (g.M + 63) / 64 * ((g.N + 127) / 128) * g.groups;
+    // cluster several SMs to a tile (128 tokens by 1024 x 4096: 10.6 against 7.9
+    // us; 100 by 4096 x 2048: 6.6 against 9.5). Rows whose starts are not 32-byte
+    // aligned cost the row kernel's loads more (float32 results of 333 tokens by
+    // 1000 x 2048: 7.3 against 9.2 us; by 1000 x 2064: 10.6 against 9.4).
+    const int64_t cols_tiles = (g.M + 63) / 64 * ft;
     if (d.nb >= 16 && (g.K % 32 == 0 ? 4 : 2) * cols_tiles <= sms)
         return launch_cols<64>(g, d, sms, s);
     // A pair's tile is four of a single block's and takes 16/9 of its time on two
-    // SMs (4096 tokens by 2048 x 4096: 39.9 us in four rounds against 35.6 in two;
-    // 1536 by 4096 x 4096: 31.0 in three against 35.0 in two).
-    const int64_t one = (g.M + 127) / 128 * ((g.N + 127) / 128) * g.groups;
+    // SMs (4096 tokens by 2048 x 4096: 40.1 us in four rounds against 35.1 in two;
+    // 1536 by 4096 x 4096: 31.0 in three against 36.3 in two).
+    const int64_t one = (g.M + 127) / 128 * ft;
     const int64_t two = (g.M + 255) / 256 * ((g.N + 255) / 256) * g.groups;
     if (16 * ((two + sms / 2 - 1) / (sms / 2)) < 9 * ((one + sms - 1) / sms))
         return launch_rows<true>(g, d, sms, s);
