@@ -318,12 +318,13 @@ def _refuse(what: str, dev: int, **operands):
 def _call_on(dev: int, fn, stream, *args):
     """Calls fn(*args, stream) with `dev` current, on its current stream when
     none is given."""
-    if dev != torch.cuda.current_device():
+    if dev != torch._C._cuda_getDevice():
         with torch.cuda.device(dev):
             return _call_on(dev, fn, stream, *args)
-    s = torch._C._cuda_getCurrentRawStream(dev) if stream is None else \
-        getattr(stream, "cuda_stream", stream)
-    _check(fn(*args, s))
+    st = fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else
+            getattr(stream, "cuda_stream", stream))
+    if st:
+        _check(st)
 
 
 def csa_add_norm_quant(x, residual=None, gamma=None, normalise: bool = True, eps: float = 1e-6,
@@ -346,7 +347,7 @@ def csa_add_norm_quant(x, residual=None, gamma=None, normalise: bool = True, eps
         _refuse("csa_add_norm_quant", dev, x=(x, _PLAIN, shape), residual=(residual, same, shape),
                 gamma=(gamma, _PLAIN[1:], (d,)), total=(total, same, shape), y=(y, same, shape),
                 codes=(codes, _CODES, shape), scale=(scale, _PLAIN[1:], blocks))
-    _call_on(dev, load().csa_add_norm_quant, stream, px, pr, pg, _DTYPE_CODE[x.dtype],
+    _call_on(dev, (_lib or load()).csa_add_norm_quant, stream, px, pr, pg, _DTYPE_CODE[x.dtype],
              x.numel() // d if d else 0, d, 1 if normalise else 0, eps, pt, py, pc, ps)
 
 
@@ -362,7 +363,7 @@ def csa_quantize_weight(W, codes, scale, stream=None):
     if not (pw and pc and ps):
         _refuse("csa_quantize_weight", dev, W=(W, _PLAIN, (N, K)), codes=(codes, _CODES, (N, K)),
                 scale=(scale, _PLAIN[1:], blocks))
-    _call_on(dev, load().csa_quantize_weight, stream, pw, _DTYPE_CODE[W.dtype], N, K, pc, ps)
+    _call_on(dev, (_lib or load()).csa_quantize_weight, stream, pw, _DTYPE_CODE[W.dtype], N, K, pc, ps)
 
 
 def csa_fp8_proj(A, A_scale, W, W_scale, out, out_scale=None, groups: int = 1, stream=None):
@@ -386,7 +387,7 @@ def csa_fp8_proj(A, A_scale, W, W_scale, out, out_scale=None, groups: int = 1, s
                 A_scale=(A_scale, _PLAIN[1:], (M, groups * nb)), W=(W, _CODES, (GN, K)),
                 W_scale=(W_scale, _PLAIN[1:], (nbo, nb)), out=(out, _DTYPE_CODE, (M, GN)),
                 out_scale=(out_scale, _PLAIN[1:], (M, nbo)))
-    _call_on(dev, load().csa_fp8_proj, stream, pa, pas, pw, pws, M, GN // groups, K, groups,
+    _call_on(dev, (_lib or load()).csa_fp8_proj, stream, pa, pas, pw, pws, M, GN // groups, K, groups,
              _DTYPE_CODE[out.dtype], po, pos)
 
 

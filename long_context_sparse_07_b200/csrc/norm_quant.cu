@@ -494,11 +494,14 @@ cudaError_t launch_norm_rows(const AddNormQuantArgs &a, int tpr, int rpb, int cu
     int dev = 0, sms = 148, per_sm = 1;
     cudaGetDevice(&dev);
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(
-        &per_sm, add_norm_quant_kernel<T, CLUSTER, MOST, RES>, tpr * rpb, 0);
-    if (e != cudaSuccess)
-        return e;
-    const int64_t want = (a.rows + rpb - 1) / rpb, room = (int64_t)sms * per_sm / ranks;
+    const int64_t want = (a.rows + rpb - 1) / rpb;
+    if (want * ranks > sms) {
+        cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(
+            &per_sm, add_norm_quant_kernel<T, CLUSTER, MOST, RES>, tpr * rpb, 0);
+        if (e != cudaSuccess)
+            return e;
+    }
+    const int64_t room = (int64_t)sms * per_sm / ranks;
     return launch_early(add_norm_quant_kernel<T, CLUSTER, MOST, RES>,
                         dim3((unsigned)((want < room ? want : room) * ranks)), tpr * rpb, 0, ranks, s,
                         (const T *)a.x, (const T *)a.residual, a.gamma,
