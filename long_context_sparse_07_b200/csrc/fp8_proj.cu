@@ -73,7 +73,7 @@ __device__ __forceinline__ uint32_t bf16_2(float a, float b)
 // - One block's tile of 128 x 256 is bound by shared memory: per block of inputs
 //   the loads write 48 KB and the MMAs read 48 KB, 750 cycles at 128 bytes a
 //   cycle where the MMAs take 512. A pair writes 32 KB in each block. 545 us
-//   became 510 us (2.16 PFLOP/s, tensor pipe 62 % busy).
+//   became 510 us (tensor pipe 62 % busy), now 494 (2.22 PFLOP/s).
 // - From an accumulator's last MMA to the next one into it pass about 1100
 //   cycles of barriers, besides its draining, which two whole-block buffers do
 //   not cover: units of half a block, with two buffers each, made 302 us of 316
@@ -91,8 +91,11 @@ __device__ __forceinline__ uint32_t bf16_2(float a, float b)
 // - Results leave through shared memory by TMA stores that run beside the next
 //   tile's products (stored from the registers, 32 rows to a store instruction, a
 //   tile's results held its epilogue for 6400 cycles).
+// - A code's quotient is the sum times the scale's reciprocal: the sum carries
+//   rounding errors of its own, and the exact quotient's two FMAs more cost 4 % of
+//   the e4m3 call above (301 against 290 us).
 // Under load the board's power cap holds the clock near 1.5 GHz: sustained, the
-// same call takes 595 us.
+// same call takes 570 to 595 us.
 template <bool PAIR> struct Rows {
     static constexpr int TN = PAIR ? 256 : 128;       // features of a tile
     static constexpr int TM = PAIR ? 256 : 128;       // tokens of a tile
@@ -483,7 +486,7 @@ proj_rows_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                 if (lead && y0 + lane < a.M && cols > 0)
                     a.out_scale[(int64_t)(y0 + lane) * a.nbo + col / 128] = sc;
                 uint32_t w[CW / 4];
-                codes_of<CW / 4>(acc, sc, w);
+                codes_of<CW / 4, false>(acc, sc, w);
 #pragma unroll
                 for (int j = 0; j < CW / 16; j++)
                     put(box, (lead ? 0 : 4) + j, w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
@@ -827,7 +830,7 @@ proj_cols_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                 m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, f));
             const float s = block_scale(m);
             uint32_t w[1];
-            codes_of<1>(p, s, w);
+            codes_of<1, false>(p, s, w);
             if (lane == 0)
                 a.out_scale[t * a.nbo + fb] = s;
             if (cols > 0)
