@@ -1056,8 +1056,13 @@ cudaError_t launch_cols(const Fp8ProjArgs &g, ProjDev d, int sms, cudaStream_t s
     const int64_t tiles = (g.M + TT - 1) / TT * ((g.N + 127) / 128) * g.groups;
     if (tiles > INT32_MAX / kMaxSplit)
         return cudaErrorInvalidConfiguration;
+    // a block to every SM, and a second one where enough blocks of inputs are left
+    // for each (16 tokens by 8192 x 8192: 20.2 against 15.3 us with two; by 4096 x
+    // 4096, four blocks each: 5.8 against 6.2)
     int split = 1;
-    while (split < kMaxSplit && tiles * split * 2 <= sms && split * 2 <= d.nb)
+    while (split < kMaxSplit && split * 2 <= d.nb &&
+           (tiles * split * 2 <= sms ||
+            (tiles * split <= sms && d.nb >= split * 2 * (TT == 64 ? 4 : 8))))
         split *= 2;
     return launch_early(proj_cols_kernel<TT>, dim3((unsigned)(tiles * split)), C::THREADS, C::SMEM,
                         split, s, tmA, tmW, d, split);
@@ -1098,11 +1103,12 @@ cudaError_t launch_fp8_proj(const Fp8ProjArgs &g, unsigned *err, cudaStream_t s)
     d.tma_out = false;
     const int sms = sm_count();
     // Up to 8 tokens take the kernel that waits least, but for e4m3 results (a
-    // scale's 128 features would have to share a block) and where the ring's
-    // kernel fills the SMs without clusters (8 tokens by 8192 x 8192: 16.6 against
-    // 19.8 us; by 20000 x 4096: 33.5 against 21.0).
+    // scale's 128 features would have to share a block), where the ring's kernel
+    // fills the SMs without clusters (8 tokens by 8192 x 1024: 3.6 against 4.3 us;
+    // by 20000 x 4096: 33.5 against 21.0) and for weights that it streams better
+    // (by 8192 x 2048: 5.0 against 5.4; by 8192 x 8192: 16.7 against 14.9).
     const int64_t ft = ((g.N + 127) / 128) * (int64_t)g.groups;
-    if (g.M <= kFewTokens && g.out_dt != CSA_E4M3 && 2 * ft <= sms)
+    if (g.M <= kFewTokens && g.out_dt != CSA_E4M3 && 2 * ft <= sms && d.ldo * g.K <= (32 << 20))
         return launch_few(g, d, sms, s);
     if (g.M <= 16)
         return launch_cols<16>(g, d, sms, s);
@@ -1110,11 +1116,12 @@ cudaError_t launch_fp8_proj(const Fp8ProjArgs &g, unsigned *err, cudaStream_t s)
         return launch_cols<32>(g, d, sms, s);
     // More tokens take the row kernel, unless long rows over few tiles leave a
     // cluster several SMs to a tile (128 tokens by 1024 x 4096: 10.6 against 7.9
-    // us; 100 by 4096 x 2048: 6.6 against 9.5). Rows whose starts are not 32-byte
-    // aligned cost the row kernel's loads more (float32 results of 333 tokens by
-    // 1000 x 2048: 7.3 against 9.2 us; by 1000 x 2064: 10.6 against 9.4).
+    // us; 100 by 4096 x 2048: 6.6 against 9.5; by 4096 x 8192: 21.6 against 17.7).
+    // Rows whose starts are not 32-byte aligned cost the row kernel's loads more
+    // (333 tokens by 1000 x 2048: 6.7 against 7.8 us; by 1000 x 2064: 9.8 against
+    // 8.8).
     const int64_t cols_tiles = (g.M + 63) / 64 * ft;
-    if (d.nb >= 16 && (g.K % 32 == 0 ? 4 : 2) * cols_tiles <= sms)
+    if (d.nb >= 16 && (g.K % 32 == 0 && d.nb < 48 ? 4 : 2) * cols_tiles <= sms)
         return launch_cols<64>(g, d, sms, s);
     // A pair's tile is four of a single block's and takes 16/9 of its time on two
     // SMs (4096 tokens by 2048 x 4096: 40.1 us in four rounds against 35.1 in two;
