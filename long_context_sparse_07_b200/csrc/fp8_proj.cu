@@ -1026,10 +1026,12 @@ cudaError_t launch_rows(const Fp8ProjArgs &g, ProjDev d, int sms, cudaStream_t s
     if (PAIR) {
         // the warpgroups' shares (regs_down, regs_up) come out of the launch's
         // registers: with fewer the epilogue would wait for ever
-        static const int regs = [] {
-            cudaFuncAttributes f;
-            return cudaFuncGetAttributes(&f, proj_rows_kernel<PAIR>) == cudaSuccess ? f.numRegs : 0;
-        }();
+        static int regs = 0;
+        cudaFuncAttributes f;
+        if (!regs && (e = cudaFuncGetAttributes(&f, proj_rows_kernel<PAIR>)) == cudaSuccess)
+            regs = f.numRegs;
+        if (e != cudaSuccess)
+            return e;
         if (regs * R::THREADS < 128 * R::REGS_DOWN + (R::THREADS - 128) * R::REGS_UP)
             return cudaErrorInvalidConfiguration;
     }

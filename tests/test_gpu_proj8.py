@@ -445,6 +445,50 @@ def test_calls_in_a_row_wait_for_each_other(n):
     abi.csa_get_error()
 
 
+def test_captured_fork_and_join():
+    """Two streams of a captured step, with copies and other kernels between the
+    calls, and a call that waits for both."""
+    n, d = 70, 512
+    gen = torch.Generator().manual_seed(3)
+    x = [torch.randn(n, d, generator=gen).to(DEV, torch.bfloat16) for _ in range(2)]
+    Wt = (torch.randn(d, d, generator=gen) / d ** 0.5).to(DEV)
+    w8, ws = torch.empty(d, d, device=DEV, dtype=F8), torch.empty(4, 4, device=DEV)
+    h = [(torch.empty(n, d, device=DEV, dtype=F8), torch.empty(n, 4, device=DEV)) for _ in x]
+    o = [torch.empty(n, d, device=DEV, dtype=torch.bfloat16) for _ in x]
+    both, out = torch.empty_like(o[0]), torch.empty(n, d, device=DEV)
+    side = torch.cuda.Stream()
+
+    def step():
+        main = torch.cuda.current_stream()
+        abi.csa_quantize_weight(Wt, w8, ws)
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            abi.csa_add_norm_quant(x[1], codes=h[1][0], scale=h[1][1])
+            abi.csa_fp8_proj(*h[1], w8, ws, o[1])
+        abi.csa_add_norm_quant(x[0], codes=h[0][0], scale=h[0][1])
+        abi.csa_fp8_proj(*h[0], w8, ws, o[0])
+        both.copy_(o[0])
+        main.wait_stream(side)
+        abi.csa_add_norm_quant(both, residual=o[1], total=both, codes=h[0][0], scale=h[0][1])
+        out.zero_()
+        abi.csa_fp8_proj(*h[0], w8, ws, out)
+
+    step()
+    torch.cuda.synchronize()
+    want = out.clone()
+    assert want.abs().max() > 1
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for _ in range(20):
+        graph.replay()
+    assert torch.equal(out, want)
+    for _ in range(20):
+        step()
+    assert torch.equal(out, want)
+    abi.csa_get_error()
+
+
 @pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
 def test_buffers_that_start_inside_a_sector(dt):
     """16-byte aligned buffers give the bits of 32-byte aligned ones."""
