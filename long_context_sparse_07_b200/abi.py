@@ -283,16 +283,18 @@ def csa_grouped_out_proj(o, Wg, Wo, g: int, u, out, stream=None):
 
 
 _PLAIN = (torch.bfloat16, torch.float32)
+_F32 = (torch.float32,)
 _CODES = (torch.float8_e4m3fn, torch.uint8)
 _DTYPE_CODE = {torch.float32: CSA_F32, torch.bfloat16: CSA_BF16, torch.float8_e4m3fn: CSA_E4M3,
                torch.uint8: CSA_E4M3}
 
 
-def _operand(t, dtypes, shape, dev):
+def _operand(t, dtypes, shape, dev, has=None):
     """Device pointer of an operand that is as a call needs it, else 0: a dense
-    tensor of a listed dtype and of this shape, on CUDA device `dev`."""
-    if (t.dtype in dtypes and t.shape == shape and t.is_contiguous() and t.get_device() == dev
-            and dev >= 0):
+    tensor of a listed dtype and of this shape, on CUDA device `dev`. `has` is
+    its shape where the caller has read it."""
+    if (t.dtype in dtypes and (has or t.shape) == shape and t.is_contiguous()
+            and t.get_device() == dev >= 0):
         return t.data_ptr() or _EMPTY
     return 0
 
@@ -336,17 +338,17 @@ def csa_add_norm_quant(x, residual=None, gamma=None, normalise: bool = True, eps
     d = shape[-1]
     same, dev = (x.dtype,), x.get_device()
     blocks = shape[:-1] + ((d + 127) >> 7,)
-    px = _operand(x, _PLAIN, shape, dev)
+    px = _operand(x, _PLAIN, shape, dev, shape)
     pr = None if residual is None else _operand(residual, same, shape, dev)
-    pg = None if gamma is None else _operand(gamma, _PLAIN[1:], (d,), dev)
+    pg = None if gamma is None else _operand(gamma, _F32, (d,), dev)
     pt = None if total is None else _operand(total, same, shape, dev)
     py = None if y is None else _operand(y, same, shape, dev)
     pc = None if codes is None else _operand(codes, _CODES, shape, dev)
-    ps = None if scale is None else _operand(scale, _PLAIN[1:], blocks, dev)
+    ps = None if scale is None else _operand(scale, _F32, blocks, dev)
     if 0 in (px, pr, pg, pt, py, pc, ps):
         _refuse("csa_add_norm_quant", dev, x=(x, _PLAIN, shape), residual=(residual, same, shape),
-                gamma=(gamma, _PLAIN[1:], (d,)), total=(total, same, shape), y=(y, same, shape),
-                codes=(codes, _CODES, shape), scale=(scale, _PLAIN[1:], blocks))
+                gamma=(gamma, _F32, (d,)), total=(total, same, shape), y=(y, same, shape),
+                codes=(codes, _CODES, shape), scale=(scale, _F32, blocks))
     _call_on(dev, (_lib or load()).csa_add_norm_quant, stream, px, pr, pg, _DTYPE_CODE[x.dtype],
              x.numel() // d if d else 0, d, 1 if normalise else 0, eps, pt, py, pc, ps)
 
@@ -357,12 +359,12 @@ def csa_quantize_weight(W, codes, scale, stream=None):
     N, K = W.shape
     dev = W.get_device()
     blocks = ((N + 127) >> 7, (K + 127) >> 7)
-    pw = _operand(W, _PLAIN, (N, K), dev)
+    pw = _operand(W, _PLAIN, (N, K), dev, (N, K))
     pc = _operand(codes, _CODES, (N, K), dev)
-    ps = _operand(scale, _PLAIN[1:], blocks, dev)
+    ps = _operand(scale, _F32, blocks, dev)
     if not (pw and pc and ps):
         _refuse("csa_quantize_weight", dev, W=(W, _PLAIN, (N, K)), codes=(codes, _CODES, (N, K)),
-                scale=(scale, _PLAIN[1:], blocks))
+                scale=(scale, _F32, blocks))
     _call_on(dev, (_lib or load()).csa_quantize_weight, stream, pw, _DTYPE_CODE[W.dtype], N, K, pc, ps)
 
 
@@ -370,23 +372,23 @@ def csa_fp8_proj(A, A_scale, W, W_scale, out, out_scale=None, groups: int = 1, s
     """out [M, groups N] = A [M, groups K] times W [groups N, K] (group by
     group), e4m3 operands with block scales; out bf16, f32, or e4m3 codes with
     out_scale [M, ceil(groups N / 128)]."""
-    M = A.shape[0]
-    GN, K = W.shape
+    a, (GN, K) = A.shape, W.shape
+    M = a[0]
     if groups < 1 or GN % groups:
         raise ValueError("csa_fp8_proj: groups must divide the rows of W")
     dev = A.get_device()
     nb, nbo = (K + 127) >> 7, (GN + 127) >> 7
-    pa = _operand(A, _CODES, (M, groups * K), dev)
-    pas = _operand(A_scale, _PLAIN[1:], (M, groups * nb), dev)
-    pw = _operand(W, _CODES, (GN, K), dev)
-    pws = _operand(W_scale, _PLAIN[1:], (nbo, nb), dev)
+    pa = _operand(A, _CODES, (M, groups * K), dev, a)
+    pas = _operand(A_scale, _F32, (M, groups * nb), dev)
+    pw = _operand(W, _CODES, (GN, K), dev, (GN, K))
+    pws = _operand(W_scale, _F32, (nbo, nb), dev)
     po = _operand(out, _DTYPE_CODE, (M, GN), dev)
-    pos = None if out_scale is None else _operand(out_scale, _PLAIN[1:], (M, nbo), dev)
+    pos = None if out_scale is None else _operand(out_scale, _F32, (M, nbo), dev)
     if not (pa and pas and pw and pws and po) or pos == 0:
         _refuse("csa_fp8_proj", dev, A=(A, _CODES, (M, groups * K)),
-                A_scale=(A_scale, _PLAIN[1:], (M, groups * nb)), W=(W, _CODES, (GN, K)),
-                W_scale=(W_scale, _PLAIN[1:], (nbo, nb)), out=(out, _DTYPE_CODE, (M, GN)),
-                out_scale=(out_scale, _PLAIN[1:], (M, nbo)))
+                A_scale=(A_scale, _F32, (M, groups * nb)), W=(W, _CODES, (GN, K)),
+                W_scale=(W_scale, _F32, (nbo, nb)), out=(out, _DTYPE_CODE, (M, GN)),
+                out_scale=(out_scale, _F32, (M, nbo)))
     _call_on(dev, (_lib or load()).csa_fp8_proj, stream, pa, pas, pw, pws, M, GN // groups, K, groups,
              _DTYPE_CODE[out.dtype], po, pos)
 
