@@ -282,6 +282,18 @@ def test_fp8_proj_matches_oracle(M, N, K, groups):
         check(out, osc, r, err, "M %d N %d K %d groups %d %s" % (M, N, K, groups, dt))
 
 
+@pytest.mark.parametrize("M,N,K", [(130, 65, 144), (601, 501, 272), (4097, 2047, 144),
+                                   (4096, 2041, 272)])
+def test_fp8_proj_result_rows_of_any_length(M, N, K):
+    """Rows that are not whole 16-byte pieces, in single tiles and in pairs'; the
+    value behind the last row stays."""
+    host = operands(M + N, M, N, K)
+    ops, (r, err) = device(*host), reference(*host, 1)
+    for dt in (torch.bfloat16, torch.float32):
+        out, _ = run(ops, N, dt, 1)
+        check(out, None, r, err, "M %d N %d K %d %s" % (M, N, K, dt))
+
+
 @pytest.mark.parametrize("M,N,K", [(5, 256, 400), (200, 300, 272), (600, 2048, 256)])
 def test_fp8_proj_zero_rows_blocks_and_special_codes(M, N, K):
     A, As, W, Ws = operands(91 + M, M, N, K)
