@@ -653,9 +653,10 @@ proj_cols_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     __syncthreads();
     tc::fence_after();
     tc::grid_let_next();
-    // the weight does not wait for the call before this one
-    if (warp == 0 && tc::elect_one())
-        for (int b = b0; b < b1; b++)
+    // the weight does not wait for the call before this one; as much as the ring
+    // holds (all of it: 12.0 against 11.0 us for 8 x 32768 x 1024 alone and cold)
+    if (warp == 4 && tc::elect_one())
+        for (int b = b0; b < b1 && b < b0 + C::STAGES; b++)
             tc::prefetch_l2_2d(&tmW, b * PB, grp * a.N + n0);
     tc::grid_wait();
     const uint32_t tmem = *tmem_slot;
