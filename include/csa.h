@@ -418,10 +418,10 @@ csa_status csa_quantize_weight(const void *W, csa_dtype dt, int64_t N, int K, vo
  *   W, W_scale  [groups N, K] e4m3 and [ceil(groups N / 128), nb] float32.
  *   out         [M, groups N] of out_dt: F32, BF16 (one rounding of r), or
  *               E4M3 with out_scale [M, ceil(groups N / 128)] float32 (the
- *               storage rule over 128 columns of r, whose quotients are good
- *               to float32: with head width 128 these
- *               are the indexer queries and their qI_scale). out_scale is NULL
- *               for the other types.
+ *               storage rule over 128 columns of r: the codes and scales that
+ *               csa_add_norm_quant gives for the float32 r; with head width
+ *               128 these are the indexer queries and their qI_scale).
+ *               out_scale is NULL for the other types.
  * A row's result does not depend on the values of other rows, and the same call
  * gives the same bits; M may choose another order of the sums.
  * Requirements: 0 <= M <= INT32_MAX (0 is a no-op); N >= 1; K a multiple of

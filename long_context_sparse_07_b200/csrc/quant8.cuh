@@ -40,10 +40,9 @@ __device__ __forceinline__ uint32_t codes_2(float2 q)
 // gives it: with r the rounded reciprocal and q = v r, q + r (v - q s) rounds
 // to the rounded quotient (P. Markstein, "Computation of elementary functions
 // on the IBM RISC System/6000 processor", 1990): three packed instructions for
-// two values. Other scales (NaN among them) divide. Without EXACT, for values
-// that carry rounding errors of their own, the quotient is v r: off by at most
-// three half steps of float32.
-template <int NW, bool EXACT = true>
+// two values. Other scales (NaN among them) divide. (v r alone turns ties
+// around: 7 x 1.5625 over a scale of 7 is 1.5625 + 2^-23, the next code up.)
+template <int NW>
 __device__ __forceinline__ void codes_of(const float2 *v, float s, uint32_t (&w)[NW])
 {
     if (s >= 0x1p-100f && s <= 0x1p100f) {
@@ -55,7 +54,7 @@ __device__ __forceinline__ void codes_of(const float2 *v, float s, uint32_t (&w)
 #pragma unroll
             for (int e = 0; e < 2; e++) {
                 const float2 x = v[2 * i + e], q = __fmul2_rn(x, r2);
-                h[e] = codes_2(EXACT ? __ffma2_rn(__ffma2_rn(q, s2, x), r2, q) : q);
+                h[e] = codes_2(__ffma2_rn(__ffma2_rn(q, s2, x), r2, q));
             }
             w[i] = h[0] | h[1] << 16;
         }

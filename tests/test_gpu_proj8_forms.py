@@ -1,0 +1,71 @@
+"""The 8-bit projections through each of their kernels: the codes' rounding.
+
+Tolerances as in test_gpu_proj8, or none: where sums are exact in float32, or
+where one call's result is another's operand, the outputs are equal bit for bit.
+"""
+import numpy as np
+import pytest
+import torch
+
+from long_context_sparse_07_b200 import abi
+from test_gpu_proj8 import DEV, F8, device, nb, operands
+
+gpu = pytest.mark.gpu
+
+
+# ---------------------------------------------------------------- e4m3 results
+
+@gpu
+@pytest.mark.parametrize("M,N,K,groups", [
+    (5, 256, 16, 1), (31, 144, 144, 1), (60, 256, 2048, 1), (700, 400, 16, 1),
+    (2300, 384, 128, 3),
+])
+def test_e4m3_results_on_a_tie_round_to_even(M, N, K, groups):
+    """Sums that are exact in float32, over scales whose reciprocals are not:
+    r = k t with a scale of k, t halfway between two codes."""
+    gen = np.random.default_rng(M)
+    base = gen.integers(8, 16, (groups * N,)) * 2.0 ** gen.integers(-7, 5, groups * N)
+    half = 2.0 ** (np.floor(np.log2(base)) - 4)      # half a step of the code
+    base[::16], half[::16] = 448.0, 0.0               # every scale's block has one
+    A = np.zeros((M, groups, K))
+    A[:, :, :2] = 1.0
+    W = np.zeros((groups * N, K))
+    W[:, 0], W[:, 1] = base, half
+
+    def f8(v):
+        t = torch.from_numpy(v).to(F8)
+        assert np.array_equal(t.double().numpy(), v)
+        return t.to(DEV)
+
+    k = np.arange(1, M + 1, dtype=np.float32)
+    As = torch.from_numpy(k).to(DEV)[:, None].expand(M, groups * nb(K)).contiguous()
+    out = torch.empty(M, groups * N, device=DEV, dtype=F8)
+    scale = torch.empty(M, nb(groups * N), device=DEV)
+    abi.csa_fp8_proj(f8(A.reshape(M, -1)), As, f8(W),
+                     torch.ones(nb(groups * N), nb(K), device=DEV), out, scale, groups=groups)
+    abi.csa_get_error()
+    assert (scale.cpu().numpy() == k[:, None]).all()
+    want = torch.from_numpy(base + half).to(F8)       # to nearest, ties to even
+    assert not np.array_equal(want.double().numpy(), base + half)
+    assert torch.equal(out.cpu().view(torch.uint8),
+                       want.view(torch.uint8)[None].expand(M, groups * N))
+
+
+@gpu
+@pytest.mark.parametrize("M,N,K,groups", [
+    (12, 512, 1024, 1), (32, 1040, 400, 1), (64, 272, 2048, 1), (1000, 2032, 272, 1),
+    (4096, 2048, 272, 1), (2300, 384, 256, 3),
+])
+def test_e4m3_results_are_the_storage_of_the_float32_results(M, N, K, groups):
+    """The same kernel's float32 results, stored by csa_add_norm_quant."""
+    ops = device(*operands(M + N, M, N, K, groups))
+    GN = groups * N
+    r = torch.empty(M, GN, device=DEV)
+    abi.csa_fp8_proj(*ops, r, groups=groups)
+    want = torch.empty(M, GN, device=DEV, dtype=F8), torch.empty(M, nb(GN), device=DEV)
+    abi.csa_add_norm_quant(r, normalise=False, codes=want[0], scale=want[1])
+    got = torch.empty_like(want[0]), torch.empty_like(want[1])
+    abi.csa_fp8_proj(*ops, *got, groups=groups)
+    abi.csa_get_error()
+    assert torch.equal(got[1], want[1])
+    assert torch.equal(got[0].view(torch.uint8), want[0].view(torch.uint8))
