@@ -437,8 +437,11 @@ csa_status csa_fp8_proj(const void *A, const float *A_scale, const void *W, cons
  * csa_debug_wait_probe -- checks the device-side failure path. Launches one
  * thread that waits, through the same bounded mbarrier wait every pipeline
  * kernel uses, on a barrier that nothing completes; after limit_ns
- * nanoseconds (1e3 .. 1e9) the wait gives up and the device error word
- * records CSA_ERR_TIMEOUT, which the next csa_get_error returns (and clears).
+ * nanoseconds (1e3 .. 1e9) the wait gives up. Then a warp waits in the form the
+ * 8-bit product's warps do, with one lane that is told to give up and a barrier
+ * that completes 0.1 s later: its lanes have to give up together. The device
+ * error word records CSA_ERR_TIMEOUT, whose second detail is the number of
+ * lanes that gave up (32); the next csa_get_error returns (and clears) it.
  * Nothing is left in flight and the device stays usable. The method has no
  * counterpart of this call: it exists so that tests can make a device wait
  * expire without faulting or hanging the GPU.

@@ -27,8 +27,8 @@
 // (13 launches) take 36.6 us so, 47.0 without the weights' prefetch and 51.2
 // with plain launches; of 32 tokens 52, 53.5 and 70 us.
 //
-// Every wait is bounded; on expiry the kernel records CSA_ERR_TIMEOUT, lets
-// its copies and products land and returns.
+// Every wait is bounded, and a warp's lanes give up together; on expiry the
+// kernel records CSA_ERR_TIMEOUT, lets its copies and products land and returns.
 #include "common.cuh"
 #include "kernels.h"
 #include "quant8.cuh"
@@ -219,7 +219,7 @@ proj_rows_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                 for (int b = 0; b < a.nb; b++, it++) {
                     const int st = it % R::STAGES;
                     if (it >= R::STAGES &&
-                        !tc::mbar_wait_sleep(&empty[st], ((it / R::STAGES) - 1) & 1, abortv)) {
+                        !tc::mbar_wait_warp(&empty[st], ((it / R::STAGES) - 1) & 1, abortv)) {
                         ok = false;
                         break;
                     }
@@ -275,7 +275,7 @@ proj_rows_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                 for (int b = 0; b < a.nb; b++, it++) {
                     const int st = it % R::STAGES;
                     if (it >= R::STAGES &&
-                        !tc::mbar_wait_sleep(&empty[st], ((it / R::STAGES) - 1) & 1, abortv)) {
+                        !tc::mbar_wait_warp(&empty[st], ((it / R::STAGES) - 1) & 1, abortv)) {
                         ok = false;
                         break;
                     }
@@ -313,10 +313,14 @@ proj_rows_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
 #pragma unroll
                 for (int h = 0; h < R::UPB; h++)
                     free[h] = it * R::UPB < R::NBUF || tc::mbar_test_wait(&acce[buf0 + h], pa);
-                ok = tc::mbar_test_wait(landed, pf) || tc::mbar_wait_sleep(landed, pf, abortv);
+                const bool in = tc::mbar_test_wait(landed, pf);
+#pragma unroll
+                for (int h = 0; h < R::UPB; h++)
+                    free[h] = tc::warp_agrees(free[h]);
+                ok = tc::warp_agrees(in) || tc::mbar_wait_warp(landed, pf, abortv);
 #pragma unroll
                 for (int h = 0; h < R::UPB; h++) {
-                    ok = ok && (free[h] || tc::mbar_wait_sleep(&acce[buf0 + h], pa, abortv));
+                    ok = ok && (free[h] || tc::mbar_wait_warp(&acce[buf0 + h], pa, abortv));
                     if (!ok)
                         break;
                     tc::fence_after();
@@ -363,7 +367,7 @@ proj_rows_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             const uint32_t total = (ntiles - first + stride - 1) / stride * a.nb;
             bool ok = true;
             for (uint32_t it = 0; it < total && ok; it++) {
-                ok = tc::mbar_wait_sleep(&scaled[it % R::SRING], (it / R::SRING) & 1, abortv);
+                ok = tc::mbar_wait_warp(&scaled[it % R::SRING], (it / R::SRING) & 1, abortv);
                 if (ok && tc::elect_one())
                     tc::mbar_arrive_cluster(tc::cluster_map(&full[it % R::FULLS], 0));
                 __syncwarp();
@@ -401,7 +405,8 @@ proj_rows_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             look();
             for (int b = 0; b < a.nb; b++) {
                 const uint32_t u = it * R::UPB + c0 / 128, buf = u % R::NBUF;
-                ok = sums || tc::mbar_wait_sleep(&accf[buf], (u / R::NBUF) & 1, abortv);
+                ok = tc::warp_agrees(sums) ||
+                     tc::mbar_wait_warp(&accf[buf], (u / R::NBUF) & 1, abortv);
                 if (!ok)
                     break;
                 tc::fence_after();
@@ -672,7 +677,7 @@ proj_cols_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         for (; it < nblk; it++) {
             const uint32_t st = it % C::STAGES;
             if (it >= C::STAGES &&
-                !tc::mbar_wait_sleep(&empty[st], ((it / C::STAGES) - 1) & 1, abortv)) {
+                !tc::mbar_wait_warp(&empty[st], ((it / C::STAGES) - 1) & 1, abortv)) {
                 if (lane == 0) {
                     *abort_flag = 1;
                     report(a.err, CSA_ERR_TIMEOUT, K_FP8_PROJ, blockIdx.x, 3);
@@ -718,9 +723,11 @@ proj_cols_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             const uint32_t st = it % C::STAGES, buf = it % C::NBUF;
             const uint32_t pa = (it / C::NBUF - 1) & 1, pf = (it / C::FULLS) & 1;
             uint64_t *landed = &full[it % C::FULLS];
-            const bool free = it < C::NBUF || tc::mbar_test_wait(&acce[buf], pa);
-            bool ok = tc::mbar_test_wait(landed, pf) || tc::mbar_wait_sleep(landed, pf, abortv);
-            ok = ok && (free || tc::mbar_wait_sleep(&acce[buf], pa, abortv));
+            const bool empty_buf = it < C::NBUF || tc::mbar_test_wait(&acce[buf], pa);
+            const bool in = tc::mbar_test_wait(landed, pf);
+            const bool free = tc::warp_agrees(empty_buf);
+            bool ok = tc::warp_agrees(in) || tc::mbar_wait_warp(landed, pf, abortv);
+            ok = ok && (free || tc::mbar_wait_warp(&acce[buf], pa, abortv));
             if (!ok) {
                 if (lane == 0) {
                     *abort_flag = 1;
@@ -757,7 +764,7 @@ proj_cols_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             acc[j] = make_float2(0.f, 0.f);
         for (uint32_t it = 0; it < nblk; it++) {
             const uint32_t buf = it % C::NBUF;
-            if (!tc::mbar_wait_sleep(&accf[buf], (it / C::NBUF) & 1, abortv)) {
+            if (!tc::mbar_wait_warp(&accf[buf], (it / C::NBUF) & 1, abortv)) {
                 *abort_flag = 1;
                 report(a.err, CSA_ERR_TIMEOUT, K_FP8_PROJ, blockIdx.x, 5);
                 break;

@@ -1,4 +1,5 @@
-"""The 8-bit projections through each of their kernels: the codes' rounding.
+"""The 8-bit projections through each of their kernels: the codes' rounding,
+waits that expire.
 
 Tolerances as in test_gpu_proj8, or none: where sums are exact in float32, or
 where one call's result is another's operand, the outputs are equal bit for bit.
@@ -69,3 +70,18 @@ def test_e4m3_results_are_the_storage_of_the_float32_results(M, N, K, groups):
     abi.csa_get_error()
     assert torch.equal(got[1], want[1])
     assert torch.equal(got[0].view(torch.uint8), want[0].view(torch.uint8))
+
+
+# ---------------------------------------------------------------- waits
+
+@gpu
+def test_lanes_of_a_warp_give_up_together():
+    """A wait that one lane of a warp gives up is given up by all 32, whatever
+    the others see (and in bounded time)."""
+    abi.load()
+    abi.csa_get_error()
+    abi.csa_debug_wait_probe(1_000_000)
+    with pytest.raises(abi.CsaError, match="kernel 8, detail 0 32") as ei:
+        abi.csa_get_error()
+    assert ei.value.status == -4
+    assert abi.csa_get_error() == 0
