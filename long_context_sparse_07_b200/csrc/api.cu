@@ -1,5 +1,6 @@
 // api.cu -- the C ABI of csa.h: argument validation, device error word and
 // dispatch to the kernel launchers. No call allocates device memory.
+#include <atomic>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -23,7 +24,7 @@ csa_status fail(csa_status st, const char *fmt, ...)
 }
 
 constexpr int kMaxDevices = 64;
-unsigned *g_err_ptr[kMaxDevices];
+std::atomic<unsigned *> g_err_ptr[kMaxDevices];      // any thread's call may be the first
 
 // Device address of this GPU's error word (looked up once per device).
 unsigned *err_word()

@@ -29,6 +29,8 @@
 //
 // Every wait is bounded, and a warp's lanes give up together; on expiry the
 // kernel records CSA_ERR_TIMEOUT, lets its copies and products land and returns.
+#include <atomic>
+
 #include "common.cuh"
 #include "kernels.h"
 #include "quant8.cuh"
@@ -1034,12 +1036,14 @@ cudaError_t launch_rows(const Fp8ProjArgs &g, ProjDev d, int sms, cudaStream_t s
     if (PAIR) {
         // the warpgroups' shares (regs_down, regs_up) come out of the launch's
         // registers: with fewer the epilogue would wait for ever
-        static int regs = 0;
-        cudaFuncAttributes f;
-        if (!regs && (e = cudaFuncGetAttributes(&f, proj_rows_kernel<PAIR>)) == cudaSuccess)
-            regs = f.numRegs;
-        if (e != cudaSuccess)
-            return e;
+        static std::atomic<int> known{0};             // any thread's call may be the first
+        int regs = known;
+        if (!regs) {
+            cudaFuncAttributes f;
+            if ((e = cudaFuncGetAttributes(&f, proj_rows_kernel<PAIR>)) != cudaSuccess)
+                return e;
+            known = regs = f.numRegs;
+        }
         if (regs * R::THREADS < 128 * R::REGS_DOWN + (R::THREADS - 128) * R::REGS_UP)
             return cudaErrorInvalidConfiguration;
     }

@@ -1,9 +1,12 @@
 """The 8-bit projections through each of their kernels: the codes' rounding,
-waits that expire.
+waits that expire, calls by several threads.
 
 Tolerances as in test_gpu_proj8, or none: where sums are exact in float32, or
 where one call's result is another's operand, the outputs are equal bit for bit.
 """
+import threading
+from concurrent.futures import ThreadPoolExecutor
+
 import numpy as np
 import pytest
 import torch
@@ -85,3 +88,34 @@ def test_lanes_of_a_warp_give_up_together():
         abi.csa_get_error()
     assert ei.value.status == -4
     assert abi.csa_get_error() == 0
+
+
+# ---------------------------------------------------------------- threads
+
+@gpu
+def test_calls_from_several_threads():
+    """Threads that call at the same time, each on its stream, through the few-token,
+    cluster, single-tile and pair kernels, get the bits of a call alone."""
+    shapes = [(5, 512, 1024, 1), (24, 512, 1024, 1), (300, 512, 512, 1), (2300, 384, 128, 3)]
+    work = []
+    for i, (M, N, K, G) in enumerate(shapes):
+        ops = device(*operands(i, M, N, K, G))
+        want = torch.empty(M, G * N, device=DEV)
+        abi.csa_fp8_proj(*ops, want, groups=G)
+        work.append((ops, G, want))
+    torch.cuda.synchronize()
+    start = threading.Barrier(8, timeout=60)
+
+    def run(t):
+        stream = torch.cuda.Stream()
+        outs = [torch.empty_like(w[2]) for w in work]
+        start.wait()
+        for r in range(20):
+            ops, G, _ = work[(t + r) % len(work)]
+            abi.csa_fp8_proj(*ops, outs[(t + r) % len(work)], groups=G, stream=stream)
+        stream.synchronize()
+        return [torch.equal(o, w[2]) for o, w in zip(outs, work)]
+
+    with ThreadPoolExecutor(8) as pool:
+        assert all(all(same) for same in pool.map(run, range(8)))
+    abi.csa_get_error()
