@@ -434,6 +434,15 @@ csa_status csa_fp8_proj(const void *A, const float *A_scale, const void *W, cons
                         float *out_scale, void *stream);
 
 /*
+ * csa_debug_fp8_proj_form -- which of its kernels a csa_fp8_proj call of these
+ * sizes takes on the current device (a B200's, without one), or a negative
+ * csa_status where it would be refused: 0 up to 8 tokens, 1 / 2 / 3 clusters
+ * over 16 / 32 / 64 tokens, 4 tiles of one block of threads, 5 tiles of a pair.
+ * So that a test can see that it reaches each of them.
+ */
+int csa_debug_fp8_proj_form(int64_t M, int N, int K, int groups, csa_dtype out_dt);
+
+/*
  * csa_debug_wait_probe -- checks the device-side failure path. Launches one
  * thread that waits, through the same bounded mbarrier wait every pipeline
  * kernel uses, on a barrier that nothing completes; after limit_ns

@@ -31,7 +31,7 @@ EXPORTS = ("csa_abi_version", "csa_status_string", "csa_last_message", "csa_comp
            "hca_dense_mqa", "csa_mqa_workspace_size", "csa_sparse_mqa_noalloc",
            "csa_noalloc_scratch_bytes", "csa_norm_rope", "csa_grouped_out_proj",
            "csa_add_norm_quant", "csa_quantize_weight", "csa_fp8_proj",
-           "csa_debug_wait_probe", "csa_get_error")
+           "csa_debug_fp8_proj_form", "csa_debug_wait_probe", "csa_get_error")
 
 
 class CsaError(RuntimeError):
@@ -105,6 +105,8 @@ def load(path: str = LIB_PATH):
     L.csa_quantize_weight.argtypes = [_P, _I, _I64, _I, _P, _P, _P]
     L.csa_fp8_proj.restype = _I
     L.csa_fp8_proj.argtypes = [_P, _P, _P, _P, _I64, _I, _I, _I, _I, _P, _P, _P]
+    L.csa_debug_fp8_proj_form.restype = _I
+    L.csa_debug_fp8_proj_form.argtypes = [_I64, _I, _I, _I, _I]
     L.csa_debug_wait_probe.restype = _I
     L.csa_debug_wait_probe.argtypes = [ctypes.c_uint64, _P]
     L.csa_get_error.restype = _I
@@ -391,6 +393,18 @@ def csa_fp8_proj(A, A_scale, W, W_scale, out, out_scale=None, groups: int = 1, s
                 out_scale=(out_scale, _F32, (M, nbo)))
     _call_on(dev, (_lib or load()).csa_fp8_proj, stream, pa, pas, pw, pws, M, GN // groups, K, groups,
              _DTYPE_CODE[out.dtype], po, pos)
+
+
+FP8_PROJ_FORMS = ("few", "cluster16", "cluster32", "cluster64", "tiles", "pairs")
+
+
+def csa_debug_fp8_proj_form(M: int, N: int, K: int, groups: int, dtype) -> str:
+    """The kernel (one of FP8_PROJ_FORMS) that csa_fp8_proj takes for M tokens,
+    N features and K inputs a group, and results of this dtype."""
+    st = load().csa_debug_fp8_proj_form(M, N, K, groups, _DTYPE_CODE[dtype])
+    if st < 0:
+        _check(st)
+    return FP8_PROJ_FORMS[st]
 
 
 def csa_debug_wait_probe(limit_ns: int, stream=None):

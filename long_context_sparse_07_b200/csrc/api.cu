@@ -102,6 +102,23 @@ csa_status check_entries(const csa_entries &t, int c, bool allow_fp8, const char
     return CSA_OK;
 }
 
+csa_status check_proj_shape(const char *w, int64_t M, int N, int K, int groups, csa_dtype out_dt)
+{
+    REQUIRE(out_dt == CSA_F32 || out_dt == CSA_BF16 || out_dt == CSA_E4M3, CSA_ERR_UNSUPPORTED,
+            "%s: output dtype must be F32, BF16 or E4M3", w);
+    REQUIRE(M >= 0 && M <= INT32_MAX && N >= 1 && groups >= 1, CSA_ERR_INVALID_ARG,
+            "%s: bad M / N / groups", w);
+    REQUIRE(K >= 16 && K % 16 == 0, CSA_ERR_UNSUPPORTED, "%s: K = %d must be a multiple of 16", w,
+            K);
+    REQUIRE((int64_t)groups * N <= kMaxFeatures && (int64_t)groups * K <= kMaxFeatures,
+            CSA_ERR_INVALID_ARG, "%s: groups N or groups K too large", w);
+    REQUIRE(groups == 1 || (N % 128 == 0 && K % 128 == 0), CSA_ERR_UNSUPPORTED,
+            "%s: several groups need N and K multiples of 128", w);
+    REQUIRE(out_dt != CSA_E4M3 || N % 16 == 0, CSA_ERR_UNSUPPORTED,
+            "%s: e4m3 output needs N a multiple of 16", w);
+    return CSA_OK;
+}
+
 }  // namespace
 
 namespace csa {
@@ -500,18 +517,9 @@ csa_status csa_fp8_proj(const void *A, const float *A_scale, const void *W, cons
                         float *out_scale, void *stream)
 {
     const char *w = "csa_fp8_proj";
-    REQUIRE(out_dt == CSA_F32 || out_dt == CSA_BF16 || out_dt == CSA_E4M3, CSA_ERR_UNSUPPORTED,
-            "%s: output dtype must be F32, BF16 or E4M3", w);
-    REQUIRE(M >= 0 && M <= INT32_MAX && N >= 1 && groups >= 1, CSA_ERR_INVALID_ARG,
-            "%s: bad M / N / groups", w);
-    REQUIRE(K >= 16 && K % 16 == 0, CSA_ERR_UNSUPPORTED, "%s: K = %d must be a multiple of 16", w,
-            K);
-    REQUIRE((int64_t)groups * N <= kMaxFeatures && (int64_t)groups * K <= kMaxFeatures,
-            CSA_ERR_INVALID_ARG, "%s: groups N or groups K too large", w);
-    REQUIRE(groups == 1 || (N % 128 == 0 && K % 128 == 0), CSA_ERR_UNSUPPORTED,
-            "%s: several groups need N and K multiples of 128", w);
-    REQUIRE(out_dt != CSA_E4M3 || N % 16 == 0, CSA_ERR_UNSUPPORTED,
-            "%s: e4m3 output needs N a multiple of 16", w);
+    const csa_status st = check_proj_shape(w, M, N, K, groups, out_dt);
+    if (st != CSA_OK)
+        return st;
     if (M == 0)
         return launched(cudaSuccess, w);
     REQUIRE(A && A_scale && W && W_scale && out, CSA_ERR_INVALID_ARG,
@@ -529,6 +537,21 @@ csa_status csa_fp8_proj(const void *A, const float *A_scale, const void *W, cons
     csa::Fp8ProjArgs a{(const uint8_t *)A, A_scale, (const uint8_t *)W, W_scale, M, N, K, groups,
                        out_dt, out, out_scale};
     return launched(csa::launch_fp8_proj(a, err, (cudaStream_t)stream), w);
+}
+
+int csa_debug_fp8_proj_form(int64_t M, int N, int K, int groups, csa_dtype out_dt)
+{
+    const csa_status st = check_proj_shape("csa_debug_fp8_proj_form", M, N, K, groups, out_dt);
+    if (st != CSA_OK)
+        return st;
+    csa::Fp8ProjArgs a{};
+    a.M = M;
+    a.N = N;
+    a.K = K;
+    a.groups = groups;
+    a.out_dt = out_dt;
+    g_msg[0] = 0;
+    return csa::fp8_proj_form(a);
 }
 
 csa_status csa_debug_wait_probe(uint64_t limit_ns, void *stream)

@@ -19,7 +19,7 @@
 // partial results are added through distributed shared memory in the order of
 // their ranks.
 // proj_few_kernel (up to 8 tokens): warp MMAs straight from global memory.
-// launch_fp8_proj says where one gives way to the next.
+// form_of says where one gives way to the next.
 //
 // All are launched so that they may start while the call before them ends (the
 // projections of a step follow one another); the two for few tokens bring their
@@ -1095,7 +1095,42 @@ cudaError_t launch_few(const Fp8ProjArgs &g, const ProjDev &d, int sms, cudaStre
                         ks * 16 * rg * kFewLd * 4, 1, s, g.A, g.W, d, ks);
 }
 
+Fp8ProjForm form_of(const Fp8ProjArgs &g, int sms)
+{
+    const int64_t nb = (g.K + PB - 1) / PB, weight = (int64_t)g.groups * g.N * g.K;
+    // Up to 8 tokens take the kernel that waits least, but for e4m3 results (a
+    // scale's 128 features would have to share a block), where the ring's kernel
+    // fills the SMs without clusters (8 tokens by 8192 x 1024: 3.6 against 4.3 us;
+    // by 20000 x 4096: 33.5 against 21.0) and for weights that it streams better
+    // (by 8192 x 2048: 5.0 against 5.4; by 8192 x 8192: 16.7 against 14.9).
+    const int64_t ft = ((g.N + 127) / 128) * (int64_t)g.groups;
+    if (g.M <= kFewTokens && g.out_dt != CSA_E4M3 && 2 * ft <= sms && weight <= (32 << 20))
+        return PROJ_FEW;
+    if (g.M <= 16)
+        return PROJ_COLS_16;
+    if (g.M <= 32)
+        return PROJ_COLS_32;
+    // More tokens take the row kernel, unless long rows over few tiles leave a
+    // cluster several SMs to a tile (128 tokens by 1024 x 4096: 10.6 against 7.9
+    // us; 100 by 4096 x 2048: 6.6 against 9.5; by 4096 x 8192: 21.6 against 17.7).
+    // Rows whose starts are not 32-byte aligned cost the row kernel's loads more
+    // (333 tokens by 1000 x 2048: 6.7 against 7.8 us; by 1000 x 2064: 9.8 against
+    // 8.8).
+    const int64_t cols_tiles = (g.M + 63) / 64 * ft;
+    if (nb >= 16 && (g.K % 32 == 0 && nb < 48 ? 4 : 2) * cols_tiles <= sms)
+        return PROJ_COLS_64;
+    // A pair's tile is four of a single block's and takes 16/9 of its time on two
+    // SMs (4096 tokens by 2048 x 4096: 40.1 us in four rounds against 35.1 in two;
+    // 1536 by 4096 x 4096: 31.0 in three against 36.3 in two).
+    const int64_t one = (g.M + 127) / 128 * ft;
+    const int64_t two = (g.M + 255) / 256 * ((g.N + 255) / 256) * g.groups;
+    return 16 * ((two + sms / 2 - 1) / (sms / 2)) < 9 * ((one + sms - 1) / sms) ? PROJ_PAIRS
+                                                                              : PROJ_TILES;
+}
+
 }  // namespace
+
+Fp8ProjForm fp8_proj_form(const Fp8ProjArgs &g) { return form_of(g, sm_count()); }
 
 cudaError_t launch_fp8_proj(const Fp8ProjArgs &g, unsigned *err, cudaStream_t s)
 {
@@ -1116,35 +1151,20 @@ cudaError_t launch_fp8_proj(const Fp8ProjArgs &g, unsigned *err, cudaStream_t s)
     d.out_dt = g.out_dt;
     d.tma_out = false;
     const int sms = sm_count();
-    // Up to 8 tokens take the kernel that waits least, but for e4m3 results (a
-    // scale's 128 features would have to share a block), where the ring's kernel
-    // fills the SMs without clusters (8 tokens by 8192 x 1024: 3.6 against 4.3 us;
-    // by 20000 x 4096: 33.5 against 21.0) and for weights that it streams better
-    // (by 8192 x 2048: 5.0 against 5.4; by 8192 x 8192: 16.7 against 14.9).
-    const int64_t ft = ((g.N + 127) / 128) * (int64_t)g.groups;
-    if (g.M <= kFewTokens && g.out_dt != CSA_E4M3 && 2 * ft <= sms && d.ldo * g.K <= (32 << 20))
+    switch (form_of(g, sms)) {
+    case PROJ_FEW:
         return launch_few(g, d, sms, s);
-    if (g.M <= 16)
+    case PROJ_COLS_16:
         return launch_cols<16>(g, d, sms, s);
-    if (g.M <= 32)
+    case PROJ_COLS_32:
         return launch_cols<32>(g, d, sms, s);
-    // More tokens take the row kernel, unless long rows over few tiles leave a
-    // cluster several SMs to a tile (128 tokens by 1024 x 4096: 10.6 against 7.9
-    // us; 100 by 4096 x 2048: 6.6 against 9.5; by 4096 x 8192: 21.6 against 17.7).
-    // Rows whose starts are not 32-byte aligned cost the row kernel's loads more
-    // (333 tokens by 1000 x 2048: 6.7 against 7.8 us; by 1000 x 2064: 9.8 against
-    // 8.8).
-    const int64_t cols_tiles = (g.M + 63) / 64 * ft;
-    if (d.nb >= 16 && (g.K % 32 == 0 && d.nb < 48 ? 4 : 2) * cols_tiles <= sms)
+    case PROJ_COLS_64:
         return launch_cols<64>(g, d, sms, s);
-    // A pair's tile is four of a single block's and takes 16/9 of its time on two
-    // SMs (4096 tokens by 2048 x 4096: 40.1 us in four rounds against 35.1 in two;
-    // 1536 by 4096 x 4096: 31.0 in three against 36.3 in two).
-    const int64_t one = (g.M + 127) / 128 * ft;
-    const int64_t two = (g.M + 255) / 256 * ((g.N + 255) / 256) * g.groups;
-    if (16 * ((two + sms / 2 - 1) / (sms / 2)) < 9 * ((one + sms - 1) / sms))
+    case PROJ_PAIRS:
         return launch_rows<true>(g, d, sms, s);
-    return launch_rows<false>(g, d, sms, s);
+    default:
+        return launch_rows<false>(g, d, sms, s);
+    }
 }
 
 }  // namespace csa

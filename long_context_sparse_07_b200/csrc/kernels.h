@@ -221,6 +221,9 @@ struct Fp8ProjArgs {
     void *out;
     float *out_scale;
 };
+// The kernel that a call takes on the current device (in csa.h's order).
+enum Fp8ProjForm { PROJ_FEW, PROJ_COLS_16, PROJ_COLS_32, PROJ_COLS_64, PROJ_TILES, PROJ_PAIRS };
+Fp8ProjForm fp8_proj_form(const Fp8ProjArgs &a);
 cudaError_t launch_fp8_proj(const Fp8ProjArgs &a, unsigned *err, cudaStream_t s);
 
 // One bounded wait that nothing completes (csa_debug_wait_probe).

@@ -1,5 +1,7 @@
-"""The 8-bit projections through each of their kernels: the codes' rounding,
-waits that expire, calls by several threads.
+"""The 8-bit product through each of its kernels (which one a call takes is asked
+of the library, so that no change of its rules leaves a kernel untested):
+results of every type, special values, the codes' rounding, waits that expire,
+calls by several threads.
 
 Tolerances as in test_gpu_proj8, or none: where sums are exact in float32, or
 where one call's result is another's operand, the outputs are equal bit for bit.
@@ -11,10 +13,70 @@ import numpy as np
 import pytest
 import torch
 
-from long_context_sparse_07_b200 import abi
-from test_gpu_proj8 import DEV, F8, device, nb, operands
+import test_gpu_proj8 as proj8
+from long_context_sparse_07_b200 import abi, build
+from test_gpu_proj8 import DEV, F8, check, device, nb, operands, reference
 
 gpu = pytest.mark.gpu
+BF, F = torch.bfloat16, torch.float32
+
+
+# ---------------------------------------------------------------- every kernel
+
+# kernel, M, N, K, groups: cut tiles and blocks on every side; several groups,
+# of whole and (384 features) half tiles of a pair. Up to 8 tokens with e4m3
+# results take the 16-token clusters.
+FORMS = [
+    ("few", 5, 300, 400, 1), ("few", 8, 128, 256, 3),
+    ("cluster16", 13, 272, 400, 1), ("cluster16", 16, 256, 128, 3),
+    ("cluster32", 31, 272, 400, 1), ("cluster32", 20, 384, 256, 2),
+    ("cluster64", 60, 272, 2064, 1), ("cluster64", 100, 128, 2048, 3),
+    ("tiles", 300, 400, 272, 1), ("tiles", 200, 384, 256, 2),
+    ("pairs", 4097, 2032, 272, 1), ("pairs", 2300, 384, 256, 3), ("pairs", 4096, 1024, 128, 2),
+]
+
+
+def form(M, N, K, groups, dt):
+    return abi.csa_debug_fp8_proj_form(M, N, K, groups, dt)
+
+
+def test_every_kernel_is_reached_with_every_result_and_groups():
+    build.build()
+    seen = {(form(M, N, K, G, dt), dt, G > 1) for _, M, N, K, G in FORMS
+            for dt in (BF, F) + ((F8,) if N % 16 == 0 else ())}
+    want = {(f, dt, g) for f in abi.FP8_PROJ_FORMS for dt in (BF, F, F8) for g in (False, True)}
+    assert seen == want - {("few", F8, False), ("few", F8, True)}
+    for bad in ((4, 128, 24, 1), (4, 120, 128, 2), (-1, 128, 128, 1), (4, 0, 128, 1)):
+        with pytest.raises(abi.CsaError):
+            form(*bad, BF)
+    with pytest.raises(abi.CsaError):
+        form(4, 24, 128, 1, F8)
+
+
+@gpu
+@pytest.mark.parametrize("kernel,M,N,K,groups", FORMS)
+def test_every_kernel_matches_oracle(kernel, M, N, K, groups):
+    host = operands(M + N + K, M, N, K, groups)
+    ops = device(*host)
+    r, err = reference(*host, groups)
+    for dt in (BF, F) + ((F8,) if N % 16 == 0 else ()):
+        assert form(M, N, K, groups, dt) == (kernel if M > 8 or dt != F8 else "cluster16")
+        out, osc = proj8.run(ops, groups * N, dt, groups)
+        check(out, osc, r, err, "%s %s" % (kernel, dt))
+
+
+# special values need two blocks of inputs, an infinite scale a last scale block
+# that is cut
+SPECIAL = [(5, 272, 400, "few"), (13, 272, 400, "cluster16"), (31, 272, 400, "cluster32"),
+           (60, 272, 2064, "cluster64"), (300, 400, 272, "tiles"), (4097, 1936, 400, "pairs")]
+
+
+@gpu
+@pytest.mark.parametrize("M,N,K,kernel", SPECIAL)
+def test_special_values_through_every_kernel(M, N, K, kernel):
+    assert form(M, N, K, 1, F) == kernel
+    proj8.test_fp8_proj_zero_rows_blocks_and_special_codes(M, N, K)
+    proj8.test_fp8_proj_infinite_rows_behind_the_last_feature(M, N, K)
 
 
 # ---------------------------------------------------------------- e4m3 results
