@@ -79,6 +79,25 @@ def test_special_values_through_every_kernel(M, N, K, kernel):
     proj8.test_fp8_proj_infinite_rows_behind_the_last_feature(M, N, K)
 
 
+@gpu
+@pytest.mark.parametrize("kernel,M,N,K,groups", FORMS)
+def test_a_rows_result_does_not_depend_on_other_rows(kernel, M, N, K, groups):
+    """Other rows' codes and scales changed, to NaN and infinity among others:
+    the rows that stay have the same bits."""
+    A, As, W, Ws = operands(M + N, M, N, K, groups)
+    gen = np.random.default_rng(K)
+    keep = np.zeros(M, bool)
+    keep[gen.choice(M, max(1, M // 5), replace=False)] = keep[M - 1] = True
+    B, Bs = gen.integers(0, 256, A.shape, dtype=np.uint8), As * gen.choice([0.0, 1e30, 3.0], As.shape)
+    Bs[gen.random(As.shape) < 0.1], Bs[gen.random(As.shape) < 0.1] = np.inf, np.nan
+    B[keep], Bs[keep] = A[keep], As[keep]
+    for dt in (BF, F) + ((F8,) if N % 16 == 0 else ()):
+        one, s1 = proj8.run(device(A, As, W, Ws), groups * N, dt, groups)
+        two, s2 = proj8.run(device(B, Bs.astype(np.float32), W, Ws), groups * N, dt, groups)
+        assert torch.equal(one[keep].view(torch.uint8), two[keep].view(torch.uint8))
+        assert dt != F8 or torch.equal(s1[keep], s2[keep])
+
+
 # ---------------------------------------------------------------- e4m3 results
 
 @gpu
