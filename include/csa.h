@@ -383,10 +383,13 @@ csa_status csa_grouped_out_proj(const void *o, const void *Wg, const void *Wo, i
  *   y         [rows, d] of dt, or NULL; may be the same buffer as x.
  *   codes     [rows, d] e4m3, and scale [rows, ceil(d / 128)] float32: both or
  *             neither. At least one of total, y and codes is given.
- * Other overlaps of outputs with inputs or outputs are not allowed. A NaN
- * makes the whole row's y and codes NaN when normalising, else the codes and
- * scale of its block; an infinity gives its block the scale +inf (and, when
- * normalising, zeros beside a NaN).
+ * Other overlaps of outputs with inputs or outputs are not allowed.
+ * NaN and infinity. When normalising, a NaN makes the whole row's y, codes and
+ * scales NaN; an infinity, whose sum of squares is infinite, gives zeros in y,
+ * codes of zero and scales of 2^-126, but a NaN in y in its own place and NaN
+ * codes and scale in its own block. Without the norm a NaN makes the codes and
+ * scale of its block NaN; an infinity gives its block the scale +inf, codes of
+ * zero and, in its own place, NaN.
  * Requirements: d a multiple of 16, 16 <= d <= 65536; eps > 0 when
  *   normalising; x, residual, total, y and codes 16-byte aligned. rows = 0 is
  *   a no-op.
