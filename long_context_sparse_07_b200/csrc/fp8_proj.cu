@@ -1071,8 +1071,11 @@ cudaError_t launch_cols(const Fp8ProjArgs &g, ProjDev d, int sms, cudaStream_t s
     if (tiles > INT32_MAX / kMaxSplit)
         return cudaErrorInvalidConfiguration;
     // a block to every SM, and a second one where enough blocks of inputs are left
-    // for each (16 tokens by 8192 x 8192: 20.2 against 15.3 us with two; by 4096 x
-    // 4096, four blocks each: 5.8 against 6.2)
+    // for each (16 tokens by 8192 x 8192: 21.2 against 19.1 us with two; by 4096 x
+    // 4096, four blocks each: 8.5 and 8.5; 64 tokens by 4096 x 8192: 16.1 against
+    // 14.3; 333 by 1000 x 2064: 9.7 and 9.7). Of the splits 1, 2, 4 and 8 the rule
+    // takes the best or one within 3 % in each of 20 sizes from 12 to 333 tokens,
+    // 512 to 12288 features and 2048 to 16384 inputs.
     int split = 1;
     while (split < kMaxSplit && split * 2 <= d.nb &&
            (tiles * split * 2 <= sms ||
@@ -1111,13 +1114,17 @@ Fp8ProjForm form_of(const Fp8ProjArgs &g, int sms)
     if (g.M <= 32)
         return PROJ_COLS_32;
     // More tokens take the row kernel, unless long rows over few tiles leave a
-    // cluster several SMs to a tile (128 tokens by 1024 x 4096: 10.6 against 7.9
-    // us; 100 by 4096 x 2048: 6.6 against 9.5; by 4096 x 8192: 21.6 against 17.7).
-    // Rows whose starts are not 32-byte aligned cost the row kernel's loads more
-    // (333 tokens by 1000 x 2048: 6.7 against 7.8 us; by 1000 x 2064: 9.8 against
-    // 8.8).
+    // cluster several SMs to a tile: four of them (128 tokens by 1024 x 2048: 8.7
+    // against 7.4 us, by 1024 x 4096: 13.1 against 9.0), or two where the rows are
+    // longer (333 tokens by 1000 x 2304: 9.2 against 9.5, x 2816: 10.2 against
+    // 10.0, x 4096: 13.1 against 11.5; the same turn between 2560 and 3200 inputs
+    // for 256 x 2048, 500 x 768, 1000 x 384, 180 x 2000, 64 x 8192 and 300 x 1280)
+    // or start off a sector of 32 bytes, which costs the row kernel's loads more
+    // (333 tokens by 1000 x 2048: 8.7 against 9.0, x 2064: 10.5 against 9.7; 256 by
+    // 2048 x 2064: 10.5 and 10.5, x 2576: 12.3 against 11.3; 1000 by 384 x 2064: 10.5
+    // against 10.0).
     const int64_t cols_tiles = (g.M + 63) / 64 * ft;
-    if (nb >= 16 && (g.K % 32 == 0 && nb < 48 ? 4 : 2) * cols_tiles <= sms)
+    if (nb >= 16 && (g.K % 32 == 0 && nb < 24 ? 4 : 2) * cols_tiles <= sms)
         return PROJ_COLS_64;
     // A pair's tile is four of a single block's and takes 16/9 of its time on two
     // SMs (4096 tokens by 2048 x 4096: 40.1 us in four rounds against 35.1 in two;

@@ -53,6 +53,14 @@ def test_every_kernel_is_reached_with_every_result_and_groups():
         form(4, 24, 128, 1, F8)
 
 
+@pytest.mark.parametrize("M,N", [(256, 2048), (333, 1000), (1000, 384), (64, 8192)])
+def test_long_or_unaligned_rows_over_few_tiles_take_clusters(M, N):
+    build.build()
+    assert form(M, N, 2048, 1, BF) == "tiles"
+    for K in (2064, 2576, 4096, 4112, 8192):
+        assert form(M, N, K, 1, BF) == "cluster64", K
+
+
 @gpu
 @pytest.mark.parametrize("kernel,M,N,K,groups", FORMS)
 def test_every_kernel_matches_oracle(kernel, M, N, K, groups):
