@@ -408,8 +408,9 @@ def csa_debug_fp8_proj_form(M: int, N: int, K: int, groups: int, dtype) -> str:
 
 
 def csa_debug_wait_probe(limit_ns: int, stream=None):
-    """Launch one bounded device wait that nothing completes; the next
-    csa_get_error() reports CSA_ERR_TIMEOUT."""
+    """Launch bounded device waits that run out (a thread's after `limit_ns`,
+    then a warp's of which one lane gives up); the next csa_get_error() reports
+    CSA_ERR_TIMEOUT."""
     _check(load().csa_debug_wait_probe(int(limit_ns), _stream(stream)))
 
 

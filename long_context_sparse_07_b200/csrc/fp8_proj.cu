@@ -71,11 +71,15 @@ __device__ __forceinline__ uint32_t bf16_2(float a, float b)
 // quarter (32 tokens) and CW features. A block's MMAs go in units of 128
 // features, of which tensor memory holds four.
 // What the form of a pair's tile answers to (grouped output projection, 16384
-// tokens x 8 groups of 4096 -> 1024, in a graph at 1965 MHz):
+// tokens x 8 groups of 4096 -> 1024, in a graph; the board's power cap holds the
+// clock near 1.55 GHz during one call, 1.2 to 1.4 during many):
 // - One block's tile of 128 x 256 is bound by shared memory: per block of inputs
 //   the loads write 48 KB and the MMAs read 48 KB, 750 cycles at 128 bytes a
 //   cycle where the MMAs take 512. A pair writes 32 KB in each block. 545 us
-//   became 510 us (tensor pipe 62 % busy), now 494 (2.22 PFLOP/s).
+//   became 510 us, now 470 to 495 (2.2 to 2.3 PFLOP/s): 806 cycles a block of
+//   inputs, with the end of its tile in them (rows of 1024 inputs: 980 in bf16,
+//   1140 in e4m3). Without the FMAs they are 754 (840, 845), without the MMAs 749
+//   (937, 1088, at 1.93 GHz), with the loads and barriers alone 659 (748, 691).
 // - From an accumulator's last MMA to the next one into it pass about 1100
 //   cycles of barriers, besides its draining, which two whole-block buffers do
 //   not cover: units of half a block, with two buffers each, made 302 us of 316
@@ -96,8 +100,7 @@ __device__ __forceinline__ uint32_t bf16_2(float a, float b)
 // - A code is the float32 sum's correctly rounded quotient, as everywhere: the
 //   sum times the scale's reciprocal alone takes two FMAs less for two values
 //   (289 against 301 us for the e4m3 call above), but turns ties around.
-// Under load the board's power cap holds the clock near 1.5 GHz: sustained, the
-// same call takes 570 to 595 us.
+// Sustained, the same call takes 550 to 590 us.
 template <bool PAIR> struct Rows {
     static constexpr int TN = PAIR ? 256 : 128;       // features of a tile
     static constexpr int TM = PAIR ? 256 : 128;       // tokens of a tile
