@@ -458,14 +458,15 @@ __device__ __forceinline__ bool mbar_try_sleep(uint64_t *bar, uint32_t parity, u
     return ok != 0;
 }
 
+// True in every lane of a converged warp if it is in all.
+__device__ __forceinline__ bool warp_agrees(bool mine) { return __all_sync(0xffffffffu, mine); }
+
 // mbar_wait of a whole warp, for a pipeline's critical loop: the lanes sleep in
 // the hardware (up to 20 us a try) instead of polling, which slows down every
 // other access to shared memory; the timer is read only after a millisecond of
 // tries. Every lane calls it and gets the same answer, by a vote: a lane that
 // judged an expiry by itself could leave the others to a warp-wide instruction
 // that it never reaches.
-__device__ __forceinline__ bool warp_agrees(bool mine) { return __all_sync(0xffffffffu, mine); }
-
 __device__ __forceinline__ bool mbar_wait_warp(uint64_t *bar, uint32_t parity, volatile int *abort)
 {
 #pragma unroll 1
