@@ -4,6 +4,7 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <initializer_list>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -43,6 +44,13 @@ unsigned *err_word()
 
 bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
 bool aligned4(const void *p) { return ((uintptr_t)p & 3u) == 0; }
+bool among(const void *p, std::initializer_list<const void *> others)
+{
+    for (const void *q : others)
+        if (p == q)
+            return true;
+    return false;
+}
 bool pow2(int64_t x) { return x > 0 && (x & (x - 1)) == 0; }
 
 // Of a projection: so that an index rounded up to a tile stays an int.
@@ -487,6 +495,8 @@ csa_status csa_add_norm_quant(const void *x, const void *residual, const float *
     REQUIRE(!y || (y != codes && y != residual), CSA_ERR_INVALID_ARG, "%s: y overlaps", w);
     REQUIRE(!codes || (codes != x && codes != residual), CSA_ERR_INVALID_ARG,
             "%s: codes must not overlap an input", w);
+    REQUIRE(!scale || !among(scale, {x, residual, gamma, total, y, codes}), CSA_ERR_INVALID_ARG,
+            "%s: scale must not overlap an operand", w);
     csa::AddNormQuantArgs a{x, residual, gamma, dt, rows, d, normalise ? 1 : 0, eps, total, y,
                             (uint8_t *)codes, scale};
     return launched(csa::launch_add_norm_quant(a, (cudaStream_t)stream), w);
@@ -508,6 +518,8 @@ csa_status csa_quantize_weight(const void *W, csa_dtype dt, int64_t N, int K, vo
     REQUIRE(aligned16(W) && aligned16(codes) && aligned4(scale), CSA_ERR_INVALID_ARG,
             "%s: W and codes must be 16-byte aligned", w);
     REQUIRE(W != codes, CSA_ERR_INVALID_ARG, "%s: codes must not overlap W", w);
+    REQUIRE(!among(scale, {W, codes}), CSA_ERR_INVALID_ARG, "%s: scale must not overlap W or codes",
+            w);
     csa::QuantWeightArgs a{W, dt, N, K, (uint8_t *)codes, scale};
     return launched(csa::launch_quantize_weight(a, (cudaStream_t)stream), w);
 }
@@ -532,6 +544,8 @@ csa_status csa_fp8_proj(const void *A, const float *A_scale, const void *W, cons
             "%s: scales must be 4-byte aligned", w);
     REQUIRE(out != A && out != W && out != A_scale && out != W_scale, CSA_ERR_INVALID_ARG,
             "%s: out must not overlap an operand", w);
+    REQUIRE(!out_scale || !among(out_scale, {A, A_scale, W, W_scale, out}), CSA_ERR_INVALID_ARG,
+            "%s: out_scale must not overlap an operand", w);
     unsigned *err = err_word();
     REQUIRE(err, CSA_ERR_CUDA, "%s: no CUDA device", w);
     csa::Fp8ProjArgs a{(const uint8_t *)A, A_scale, (const uint8_t *)W, W_scale, M, N, K, groups,
